@@ -63,7 +63,10 @@ enum em_option {
     EM_OPT_LAW = 6,              /* 0 "throughput" law (1); 1 "quality" law (2); 2 "auto"
                                     (default): quality for d <= 16, else throughput (README
                                     `batch_law`, "Note on low dimension")                      */
-    EM_OPT_INPUT_DTYPE = 7,      /* dtype of X: 0 fp32 (default), 1 bf16                       */
+    EM_OPT_INPUT_DTYPE = 7,      /* dtype of X: 0 fp32 (default), 1 bf16, 3 a block8 matrix: X is
+                                    then a const em_block8_t* (host memory) of d columns and at
+                                    least n rows, whose rows [0, n) are read back to bf16 (which
+                                    is exact) inside the call                                   */
     EM_OPT_CHECK_FINITE = 8,     /* 1: scan X for NaN/Inf in em_begin/em_train (EM_E_NONFINITE) */
     EM_OPT_WAIT_LIMIT_MS = 9,    /* limit of every device-side spin wait, ms (default 2000)    */
     EM_OPT_AUTO_REVIVE = 10,     /* 1 (default): em_step runs the revival check after every 5th
@@ -374,6 +377,85 @@ int em_selftest(em_model* m, int which, double wait_ms);
  * values, host or device pointer, may be NULL) and the power-of-two scale.
  * EM_E_STATE before any fit. */
 int em_fp8_converter(const em_model* m, float* shift, float* scale);
+
+/* ---- block-scaled FP8 matrices ----
+ *
+ * (The pages have no counterpart: their FP8 format, EM_OPT_SEARCH_FORMAT, has one
+ * scale for all data and lives inside the search.) A block8 matrix holds rows of d
+ * values as E4M3 codes with one power-of-two scale for each block of 128 values along
+ * the row: half the memory of bf16, for vectors that stay resident. With a the largest
+ * magnitude among a block's finite values, its exponent e is the smallest integer with
+ * a <= 448 * 2^e, within [-117, 119] (0 if a = 0); a value x is held as the code
+ * e4m3(x * 2^-e), rounded to nearest even, and stands for code * 2^e (values beyond
+ * 448 * 2^119, near fp32's largest, saturate there). NaN and infinities are held as
+ * NaN.
+ *
+ * The caller owns all memory (em_block8_t holds device pointers), and nothing is
+ * allocated: the calls can be captured into CUDA graphs. All pointers of a call are
+ * device memory of one device (host pointers: EM_E_INVAL), whichever device is
+ * current. Work is ordered on `stream`, a cudaStream_t of that device (NULL = the
+ * legacy default stream), and no call but em_block8_check waits for it. Calls that
+ * write rows which another call in flight reads or writes must be ordered by the
+ * caller. Counts of 0 are accepted and do nothing.
+ *
+ * Layout. codes: rows of pitch = round_up(d, 16) bytes, zero from d on, 16-byte
+ * aligned. scales: bytes e + 127; that of (row, block = column / 128) is at
+ *   ((((row / 128) * G + block / 4) * 32 + row % 32) * 4 + (row / 32) % 4) * 4 + block % 4
+ * with G = ceil(ceil(d / 128) / 4), 16-byte aligned; bytes of blocks past the last are
+ * unused. Rows never written stand for whatever the memory holds (zero-filled codes:
+ * zeros). */
+typedef struct em_block8_t {
+    void* codes;     /* code_bytes of em_block8_layout                                        */
+    void* scales;    /* scale_bytes of em_block8_layout                                       */
+    int32_t* claims; /* `rows` entries, any content: needed to write by slots with n > 512, else
+                        may be NULL (a call that writes by slots uses it as scratch)          */
+    int32_t* status; /* one word, zero at first: device-side errors (em_block8_check)         */
+    int64_t rows;    /* 1 <= rows < 2^31                                                      */
+    int64_t d;       /* 1 <= d <= 2^24                                                        */
+} em_block8_t;
+
+/* element types of X and of results (EM_OPT_INPUT_DTYPE takes 0, 1 and 3) */
+#define EM_DTYPE_F32 0
+#define EM_DTYPE_BF16 1
+#define EM_DTYPE_F16 2
+#define EM_DTYPE_BLOCK8 3
+
+/* Sizes of a rows x d matrix (host code; any output may be NULL). */
+int em_block8_layout(int64_t rows, int64_t d, int64_t* pitch, int64_t* code_bytes, int64_t* scale_bytes);
+
+/* Quantises X, n rows of m->d values of type dtype (0 fp32, 1 bf16, 2 fp16), into rows
+ * [first, first + n) of the matrix, or, with slots (n int64 on the device; first is
+ * then 0), row i into row slots[i]. Slot -1 leaves row i out (padding); another slot
+ * outside [0, rows) leaves it out and raises EM_E_BOUNDS; of rows that name the same
+ * slot the last stays. Rows that the call does not name are left as they are. Value j
+ * of row i is X[i * row_stride + j * col_stride] (strides in elements): one of the two
+ * is 1, so a matrix and the transpose of one are both taken as they lie (row_stride 0
+ * repeats one row); 16-byte aligned rows load fastest. */
+int em_block8_write(const em_block8_t* m, const void* X, int dtype, int64_t n, int64_t row_stride, int64_t col_stride,
+                    int64_t first, const int64_t* slots, void* stream);
+
+/* Reads n rows back, [first, first + n) or slots[i] (first is then 0), to rows of `out`
+ * (d values of type dtype, row_stride >= d elements apart). fp32 and bf16 are exact;
+ * fp16 rounds to nearest even. Slot -1 reads as zeros; another slot outside
+ * [0, rows) does too, and raises EM_E_BOUNDS. Values between d and row_stride are left
+ * as they are. */
+int em_block8_read(const em_block8_t* m, int64_t first, const int64_t* slots, int64_t n, void* out, int dtype,
+                   int64_t row_stride, void* stream);
+
+/* out[i * row_stride + j] = sum over t of a[i][t] * b[j][t] for rows [0, na) of a and
+ * [0, nb) of b, which have the same d: products of the held values, exact, summed in
+ * fp32 on the tensor cores and rounded once to dtype. `out` overlaps neither matrix.
+ * The result for a row holding NaN is NaN and no other row's is touched. Device-side
+ * errors are raised in a's status word.
+ * Gradients of out = A B^T for dOut (na x nb) are two more such products: dA = dOut B
+ * with matrices written from dOut and from B's transpose, dB = dOut^T A with matrices
+ * written from dOut's and from A's transposes (em_block8_write with row_stride 1). */
+int em_block8_matmul(const em_block8_t* a, int64_t na, const em_block8_t* b, int64_t nb, void* out, int dtype,
+                     int64_t row_stride, void* stream);
+
+/* Waits for `stream` and reports a device-side error raised in the matrix's status
+ * word since the last check (EM_E_BOUNDS, EM_E_TIMEOUT), which it clears. */
+int em_block8_check(const em_block8_t* m, void* stream);
 
 /* ---- data parallelism (README "Several GPUs": DistributedEmeans) ----
  *

@@ -53,6 +53,11 @@ EM_OPT_PREFETCH = 17
 EM_OPT_SEARCH_FORMAT = 18
 EM_OPT_PDL = 19
 
+EM_DTYPE_F32 = 0
+EM_DTYPE_BF16 = 1
+EM_DTYPE_F16 = 2
+EM_DTYPE_BLOCK8 = 3
+
 EM_PHASE_PREPARE = 0
 EM_PHASE_GATHER = 1
 EM_PHASE_ASSIGN = 2
@@ -115,8 +120,16 @@ class em_profile_t(ctypes.Structure):
         }
 
 
+class em_block8_t(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("claims", ctypes.c_void_p),
+        ("status", ctypes.c_void_p), ("rows", ctypes.c_int64), ("d", ctypes.c_int64),
+    ]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
+_B8 = ctypes.POINTER(em_block8_t)
 _SIGS = {
     "em_last_error": (ctypes.c_char_p, []),
     "em_device_count": (ctypes.c_int, []),
@@ -155,6 +168,11 @@ _SIGS = {
     "em_sync": (ctypes.c_int, [_P]),
     "em_selftest": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_double]),
     "em_fp8_converter": (ctypes.c_int, [_P, _P, ctypes.POINTER(ctypes.c_float)]),
+    "em_block8_layout": (ctypes.c_int, [_I64, _I64] + [ctypes.POINTER(_I64)] * 3),
+    "em_block8_write": (ctypes.c_int, [_B8, _P, ctypes.c_int, _I64, _I64, _I64, _I64, _P, _P]),
+    "em_block8_read": (ctypes.c_int, [_B8, _I64, _P, _I64, _P, ctypes.c_int, _I64, _P]),
+    "em_block8_matmul": (ctypes.c_int, [_B8, _I64, _B8, _I64, _P, ctypes.c_int, _I64, _P]),
+    "em_block8_check": (ctypes.c_int, [_B8, _P]),
     "em_dp_unique_id": (ctypes.c_int, [_P]),
     "em_dp_init": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int, _P]),
     "em_dp_world": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]),
@@ -191,9 +209,11 @@ def check(rc: int, where: str = "call") -> None:
 
 
 def _ptr(x):
-    """Address of a tensor / ndarray / raw int (0 for None)."""
+    """Address of a tensor / ndarray / raw int (0 for None); of a Block8's C struct."""
     if x is None:
         return None
+    if isinstance(x, Block8):
+        return ctypes.addressof(x.view)
     if isinstance(x, int):
         return x
     if hasattr(x, "data_ptr"):
@@ -247,6 +267,131 @@ def dp_schedule(n_local, k, epochs, world, rank, count, law=0, batch_size=0, alp
     return tuple(out)
 
 
+def block8_layout(rows, d):
+    """(pitch, code bytes, scale bytes) of a rows x d block8 matrix (host code)."""
+    out = [_I64() for _ in range(3)]
+    check(em_block8_layout(int(rows), int(d), *(ctypes.byref(o) for o in out)), "em_block8_layout")
+    return tuple(o.value for o in out)
+
+
+class Block8:
+    """A rows x d matrix held as E4M3 codes with a power-of-two scale per block of 128
+    values of a row (em_block8_t in include/emeans.h says what is held and where).
+
+    The memory is torch tensors: `codes` (rows x pitch, uint8), `scales` (uint8, in the
+    order of the header), `claims` and `status` (scratch). `codes` and `scales` may be
+    given, filled or not; otherwise they are made and stand for zeros. The calls run on
+    `stream` (a torch.cuda.Stream; by default the current stream of the matrix's device)
+    and do not wait for it. A Block8 is also an X for Model.train, begin, lloyd, assign
+    and mse."""
+
+    def __init__(self, rows, d, device=None, codes=None, scales=None):
+        import torch
+
+        pitch, code_bytes, scale_bytes = block8_layout(rows, d)
+        given = codes if codes is not None else scales
+        if device is None:
+            device = given.device if given is not None else torch.device("cuda", torch.cuda.current_device())
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.rows, self.d, self.pitch = int(rows), int(d), pitch
+        for name, t, n in (("codes", codes, code_bytes), ("scales", scales, scale_bytes)):
+            if t is not None and (t.dtype != torch.uint8 or t.numel() != n or not t.is_contiguous()
+                                  or t.device != self.device):
+                raise ValueError(f"{name} must be {n} contiguous uint8 values on {self.device}")
+        self.codes = (torch.zeros(self.rows, pitch, dtype=torch.uint8, device=self.device) if codes is None
+                      else codes.view(self.rows, pitch))
+        self.scales = (torch.full((scale_bytes,), 127, dtype=torch.uint8, device=self.device) if scales is None
+                       else scales.view(-1))
+        self.claims = torch.empty(self.rows, dtype=torch.int32, device=self.device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.view = em_block8_t(self.codes.data_ptr(), self.scales.data_ptr(), self.claims.data_ptr(),
+                                self.status.data_ptr(), self.rows, self.d)
+        self._ref = ctypes.byref(self.view)
+
+    @property
+    def shape(self):
+        return (self.rows, self.d)
+
+    def _stream(self, stream):
+        if stream is None:
+            import torch
+
+            stream = torch.cuda.current_stream(self.device)
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def _matrix(self, t, cols, name):
+        """Type code and element strides of a 2-D tensor of `cols` columns on this device."""
+        dtype = _DTYPES.get(str(t.dtype))
+        if dtype is None:
+            raise TypeError(f"{name} must be float32, bfloat16 or float16, not {t.dtype}")
+        if t.dim() != 2 or t.shape[1] != cols:
+            raise ValueError(f"{name} must be 2-D with {cols} columns, not {tuple(t.shape)}")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the matrix on {self.device}")
+        rs, cs = t.stride()
+        # a dimension of one element has no stride of its own
+        if cols == 1:
+            cs = 1
+        if t.shape[0] == 1 and cs != 1:
+            rs = 1
+        return dtype, rs, cs
+
+    def _slots(self, slots, n, first):
+        if slots is None:
+            return None
+        if str(slots.dtype) != "torch.int64" or slots.dim() != 1 or not slots.is_contiguous():
+            raise ValueError("slots must be a contiguous 1-D int64 tensor")
+        if len(slots) != n:
+            raise ValueError(f"{len(slots)} slots for {n} rows")
+        if slots.device != self.device:
+            raise ValueError(f"slots are on {slots.device}, the matrix on {self.device}")
+        if first:
+            raise ValueError("first must be 0 with slots")
+        return slots.data_ptr() if n else None
+
+    def write(self, X, first=0, slots=None, stream=None):
+        """Quantises X (n x d; row- or column-contiguous) into rows first, first + 1, ...,
+        or into rows slots[i] (-1: not written; the last of equal slots stays)."""
+        dtype, rs, cs = self._matrix(X, self.d, "X")
+        n = X.shape[0]
+        slots = self._slots(slots, n, first)
+        check(em_block8_write(self._ref, X.data_ptr(), dtype, n, rs, cs, int(first), slots, self._stream(stream)),
+              "em_block8_write")
+
+    def read(self, out, first=0, slots=None, stream=None):
+        """Reads out.shape[0] rows from `first` on, or rows slots[i] (-1: zeros), into out."""
+        dtype, rs, cs = self._matrix(out, self.d, "out")
+        n = out.shape[0]
+        if cs != 1 and n:
+            raise ValueError("the rows of out must be contiguous")
+        slots = self._slots(slots, n, first)
+        check(em_block8_read(self._ref, int(first), slots, n, out.data_ptr(), dtype, rs if n > 1 else self.d,
+                             self._stream(stream)), "em_block8_read")
+        return out
+
+    def matmul(self, other, out, stream=None):
+        """out[i, j] = row i of this matrix . row j of `other`, for out's shape."""
+        dtype, rs, cs = self._matrix(out, out.shape[-1], "out")
+        if other.device != self.device:
+            raise ValueError(f"the other matrix is on {other.device}, this one on {self.device}")
+        na, nb = out.shape
+        if cs != 1 and na and nb:
+            raise ValueError("the rows of out must be contiguous")
+        check(em_block8_matmul(self._ref, na, other._ref, nb, out.data_ptr(), dtype, rs if na > 1 else nb,
+                               self._stream(stream)), "em_block8_matmul")
+        return out
+
+    def check(self, stream=None):
+        """Waits for the stream; raises EmeansError for a device-side error (a slot
+        outside the matrix) since the last check."""
+        check(em_block8_check(self._ref, self._stream(stream)), "em_block8_check")
+
+
+_DTYPES = {"torch.float32": EM_DTYPE_F32, "torch.bfloat16": EM_DTYPE_BF16, "torch.float16": EM_DTYPE_F16}
+
+
 def exchange_dp_id(group=None):
     """(world, rank, id): rank 0 of a torch.distributed group makes a communicator id
     and broadcasts it to the group's other ranks."""
@@ -260,7 +405,8 @@ def exchange_dp_id(group=None):
 
 
 class Model:
-    """One e-means model (handle owner). X and outputs are torch tensors or pointers."""
+    """One e-means model (handle owner). X and outputs are torch tensors or pointers; X
+    may be a Block8."""
 
     def __init__(self, d: int, k: int, seed: int = 1234, **options):
         h = em_create(int(d), int(k), int(seed))
@@ -268,6 +414,7 @@ class Model:
             raise EmeansError(em_last_error_code() or EM_E_INVAL, "em_create")
         self.h = h
         self.d, self.k, self.seed = int(d), int(k), int(seed)
+        self._raw_dtype = None
         for name, value in options.items():
             self.set_option(name, value)
 
@@ -289,7 +436,7 @@ class Model:
         if name == "law" and isinstance(value, str):
             value = {"throughput": 0, "quality": 1, "auto": 2}[value]
         if name == "input_dtype" and not isinstance(value, (int, float)):
-            value = 1 if "bfloat16" in str(value) or str(value) == "bf16" else 0
+            value = 1 if "bfloat16" in str(value) or str(value) == "bf16" else 3 if str(value) == "block8" else 0
         check(em_set_option(self.h, self._OPTS[name], float(value)), f"em_set_option({name})")
 
     def get_option(self, name) -> float:
@@ -298,8 +445,15 @@ class Model:
         return v.value
 
     def _dtype_of(self, X):
-        if hasattr(X, "dtype"):
+        was = int(self.get_option("input_dtype"))
+        if isinstance(X, Block8):
+            if was != EM_DTYPE_BLOCK8:
+                self._raw_dtype = was  # what a raw pointer points to
+            self.set_option("input_dtype", EM_DTYPE_BLOCK8)
+        elif hasattr(X, "dtype"):
             self.set_option("input_dtype", 1 if "bfloat16" in str(X.dtype) else 0)
+        elif was == EM_DTYPE_BLOCK8 and self._raw_dtype is not None:
+            self.set_option("input_dtype", self._raw_dtype)
 
     def set_stream(self, stream):
         check(em_set_stream(self.h, stream), "em_set_stream")

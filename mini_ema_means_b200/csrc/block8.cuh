@@ -1,0 +1,332 @@
+// block8.cuh -- host side of the block-scaled FP8 matrices (k_block8.cuh): argument
+// checks, launch shapes and the C ABI. Included at the end of emeans.cu.
+#pragma once
+
+namespace {
+
+// Makes a device current for a call and puts the caller's back.
+struct DeviceGuard {
+    int prev = -1;
+    cudaError_t to(int dev) {
+        cudaError_t e = cudaGetDevice(&prev);
+        if (e != cudaSuccess || prev == dev) {
+            prev = -1;
+            return e;
+        }
+        return cudaSetDevice(dev);
+    }
+    ~DeviceGuard() {
+        if (prev >= 0) cudaSetDevice(prev);
+    }
+};
+
+// The device a pointer's memory is on, or -1 for host memory (and what is no memory).
+int device_of(const void* p) {
+    cudaPointerAttributes a;
+    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+        cudaGetLastError();
+        return -1;
+    }
+    return a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged ? a.device : -1;
+}
+
+// Every given pointer on one device (NULL ones are not asked). *dev: that device.
+int same_device(const char* what, const void* const* ptrs, int count, int* dev) {
+    *dev = -1;
+    for (int i = 0; i < count; ++i) {
+        if (!ptrs[i]) continue;
+        const int d = device_of(ptrs[i]);
+        if (d < 0 && em_device_count() < 1) return fail(EM_E_NODEVICE, "no CUDA device");
+        if (d < 0) return fail(EM_E_INVAL, "%s takes device pointers only", what);
+        if (*dev >= 0 && d != *dev) return fail(EM_E_INVAL, "%s: memory of two devices (%d and %d)", what, *dev, d);
+        *dev = d;
+    }
+    return EM_OK;
+}
+
+constexpr int64_t kB8MaxD = 1ll << 24;
+
+int64_t b8_pitch(int64_t d) { return (d + 15) / 16 * 16; }
+int64_t b8_blocks(int64_t d) { return (d + b8::kBlock - 1) / b8::kBlock; }
+int64_t b8_groups(int64_t d) { return (b8_blocks(d) + 3) / 4; }
+
+int b8_check_shape(int64_t rows, int64_t d) {
+    if (rows < 1 || rows >= (1ll << 31) || d < 1 || d > kB8MaxD)
+        return fail(EM_E_INVAL, "a block8 matrix needs 1 <= rows < 2^31 and 1 <= d <= 2^24 (rows %lld, d %lld)",
+                    (long long)rows, (long long)d);
+    return EM_OK;
+}
+
+int b8_check(const em_block8_t* m) {
+    if (!m) return fail(EM_E_INVAL, "the block8 matrix is NULL");
+    CKR(b8_check_shape(m->rows, m->d));
+    if (!m->codes || !m->scales || !m->status)
+        return fail(EM_E_INVAL, "a block8 matrix needs codes, scales and a status word");
+    if (((uintptr_t)m->codes & 15) || ((uintptr_t)m->scales & 15) || ((uintptr_t)m->status & 3) ||
+        ((uintptr_t)m->claims & 3))
+        return fail(EM_E_INVAL, "block8 codes and scales must be 16-byte aligned, status and claims 4-byte aligned");
+    return EM_OK;
+}
+
+size_t dtype_size(int dtype) { return dtype == EM_DTYPE_F32 ? 4 : 2; }
+
+int b8_check_dtype(int dtype, const void* p, const char* what) {
+    if (dtype != EM_DTYPE_F32 && dtype != EM_DTYPE_BF16 && dtype != EM_DTYPE_F16)
+        return fail(EM_E_INVAL, "dtype is 0 (fp32), 1 (bf16) or 2 (fp16), not %d", dtype);
+    if ((uintptr_t)p % dtype_size(dtype)) return fail(EM_E_INVAL, "%s is not aligned to its type", what);
+    return EM_OK;
+}
+
+// Rows [first, first + n) or slots; n within the limits of the row indexes.
+int b8_check_rows(const em_block8_t* m, int64_t first, const int64_t* slots, int64_t n) {
+    if (n < 0 || n >= (1ll << 31)) return fail(EM_E_INVAL, "need 0 <= n < 2^31 (n = %lld)", (long long)n);
+    if (slots) {
+        if (first != 0) return fail(EM_E_INVAL, "first must be 0 with slots");
+        if ((uintptr_t)slots & 7) return fail(EM_E_INVAL, "slots must be 8-byte aligned");
+    } else if (first < 0 || first > m->rows - n) {
+        return fail(EM_E_INVAL, "rows [%lld, %lld) are outside the matrix's %lld rows", (long long)first,
+                    (long long)(first + n), (long long)m->rows);
+    }
+    return EM_OK;
+}
+
+struct DeviceFacts {
+    int sms = 0, clock_khz = 0;
+    bool smem_set = false;
+};
+std::mutex g_b8_mu;
+DeviceFacts g_b8_dev[64];
+
+template <int BN, int OB, bool SWAP>
+bool b8_smem_attribute() {
+    return cudaFuncSetAttribute(b8::k_block8_matmul<BN, OB, SWAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                b8::MmCfg<BN>::kSmemBytes) == cudaSuccess;
+}
+
+// The current device's SM count and clock; on the first call, its kernels' shared
+// memory limits too.
+int b8_device(int dev, DeviceFacts* out) {
+    if (dev < 0 || dev >= 64) return fail(EM_E_INVAL, "device index out of range");
+    std::lock_guard<std::mutex> lock(g_b8_mu);
+    DeviceFacts& f = g_b8_dev[dev];
+    if (!f.smem_set) {
+        int major = 0, minor = 0;
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+        if (major != 10 || minor != 0) return fail(EM_E_NODEVICE, "this library is built for sm_100a (B200)");
+        CK(cudaDeviceGetAttribute(&f.sms, cudaDevAttrMultiProcessorCount, dev));
+        CK(cudaDeviceGetAttribute(&f.clock_khz, cudaDevAttrClockRate, dev));
+        if (!b8_smem_attribute<128, 4, false>() || !b8_smem_attribute<128, 2, false>() ||
+            !b8_smem_attribute<128, 4, true>() || !b8_smem_attribute<128, 2, true>()) {
+            cudaGetLastError();
+            return fail(EM_E_CUDA, "cudaFuncSetAttribute failed");
+        }
+        f.smem_set = true;
+    }
+    *out = f;
+    return EM_OK;
+}
+
+template <class T>
+cudaError_t b8_launch_write(bool cols, int grid, cudaStream_t st, const void* X, int64_t n, int64_t d, int64_t ldx,
+                            int vec_ok, const int64_t* slots, int64_t first, const int* claims, const em_block8_t* m) {
+    return launch_k(true, cols ? b8::k_block8_write_cols<T> : b8::k_block8_write<T>, dim3(grid), dim3(256), 0, st,
+                    static_cast<const T*>(X), n, d, ldx, vec_ok, slots, first, claims, static_cast<uint8_t*>(m->codes),
+                    static_cast<uint8_t*>(m->scales), m->rows, b8_pitch(d), m->status);
+}
+
+template <class T>
+cudaError_t b8_launch_read(int grid, cudaStream_t st, const em_block8_t* m, const int64_t* slots, int64_t first,
+                           int64_t n, void* out, int64_t ldo, int64_t width, int vec_ok) {
+    return launch_k(true, b8::k_block8_read<T>, dim3(grid), dim3(256), 0, st,
+                    static_cast<const uint8_t*>(m->codes), static_cast<const uint8_t*>(m->scales), m->rows,
+                    b8_pitch(m->d), m->d, slots, first, n, static_cast<T*>(out), ldo, width, vec_ok, m->status);
+}
+
+// Reads rows with no checks but the kernel's own (`width` columns per row).
+int b8_read(const em_block8_t* m, int64_t first, const int64_t* slots, int64_t n, void* out, int dtype, int64_t ldo,
+            int64_t width, int sms, cudaStream_t st) {
+    const int64_t pairs = n * b8_blocks(m->d);
+    const int grid = grid_for((pairs + 3) / 4 * 32, 256, sms, 8);
+    const int vec_ok = (uintptr_t)out % (4 * dtype_size(dtype)) == 0 && ldo % 4 == 0;
+    switch (dtype) {
+        case EM_DTYPE_F32: CK(b8_launch_read<float>(grid, st, m, slots, first, n, out, ldo, width, vec_ok)); break;
+        case EM_DTYPE_BF16:
+            CK(b8_launch_read<__nv_bfloat16>(grid, st, m, slots, first, n, out, ldo, width, vec_ok));
+            break;
+        default: CK(b8_launch_read<__half>(grid, st, m, slots, first, n, out, ldo, width, vec_ok)); break;
+    }
+    return EM_OK;
+}
+
+}  // namespace
+
+// The rows [0, n) of a block8 matrix as a model's bf16 data (pitch m->ld, zeros past d).
+static int read_block8(em_model* m, const em_block8_t* x, int64_t n, __nv_bfloat16* out) {
+    CKR(b8_check(x));
+    if (x->d != m->d || n > x->rows)
+        return fail(EM_E_INVAL, "the block8 matrix is %lld x %lld: the model needs %lld rows of %lld values",
+                    (long long)x->rows, (long long)x->d, (long long)n, (long long)m->d);
+    const void* ptrs[] = {x->codes, x->scales, x->status};
+    int dev;
+    CKR(same_device("a block8 input", ptrs, 3, &dev));
+    if (dev != m->dev) return fail(EM_E_INVAL, "the block8 matrix is on device %d, the model on %d", dev, m->dev);
+    return b8_read(x, 0, nullptr, n, out, EM_DTYPE_BF16, m->ld, m->ld, m->sms, m->stream);
+}
+
+namespace {
+
+template <int BN, int OB, bool SWAP>
+int b8_launch_matmul(const em_block8_t* a, const em_block8_t* b, b8::MmArgs p, int sms, cudaStream_t st) {
+    CUtensorMap tmA, tmB;
+    CKR(make_tmap8(&tmA, a->codes, a->rows, (int)a->d, (int)b8_pitch(a->d), 128));
+    CKR(make_tmap8(&tmB, b->codes, b->rows, (int)b->d, (int)b8_pitch(b->d), BN));
+    p.sfa = static_cast<const uint8_t*>(a->scales);
+    p.sfb = static_cast<const uint8_t*>(b->scales);
+    p.n_atoms = (b->rows + 127) / 128;
+    p.nkb = (int)b8_blocks(a->d);
+    p.m_tiles = (int)((p.m_rows + 127) / 128);
+    p.n_tiles = (int)((p.n_rows + BN - 1) / BN);
+    const int grid = (int)std::min<int64_t>((int64_t)p.m_tiles * p.n_tiles, sms);
+    CK(launch_k(true, b8::k_block8_matmul<BN, OB, SWAP>, dim3(grid), dim3(b8::kMmThreads), b8::MmCfg<BN>::kSmemBytes, st,
+                tmA, tmB, p));
+    return EM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int em_block8_layout(int64_t rows, int64_t d, int64_t* pitch, int64_t* code_bytes, int64_t* scale_bytes) {
+    CKR(b8_check_shape(rows, d));
+    if (pitch) *pitch = b8_pitch(d);
+    if (code_bytes) *code_bytes = rows * b8_pitch(d);
+    if (scale_bytes) *scale_bytes = (rows + 127) / 128 * b8_groups(d) * b8::kAtomBytes;
+    return EM_OK;
+}
+
+int em_block8_write(const em_block8_t* m, const void* X, int dtype, int64_t n, int64_t row_stride, int64_t col_stride,
+                    int64_t first, const int64_t* slots, void* stream) {
+    CKR(b8_check(m));
+    CKR(b8_check_dtype(dtype, X, "X"));
+    CKR(b8_check_rows(m, first, slots, n));
+    if (row_stride < 0 || col_stride < 0 || (row_stride != 1 && col_stride != 1))
+        return fail(EM_E_INVAL, "one of row_stride and col_stride must be 1, and neither negative");
+    if (n == 0) return EM_OK;
+    if (!X) return fail(EM_E_INVAL, "X is NULL");
+    if (slots && n > b8::kScanRows && !m->claims)
+        return fail(EM_E_INVAL, "writing more than %d rows by slots needs the matrix's claims array", b8::kScanRows);
+    const void* ptrs[] = {m->codes, m->scales, m->claims, m->status, X, slots};
+    int dev;
+    CKR(same_device("em_block8_write", ptrs, 6, &dev));
+    DeviceGuard guard;
+    CK(guard.to(dev));
+    DeviceFacts f;
+    CKR(b8_device(dev, &f));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int* claims = nullptr;
+    if (slots && n > b8::kScanRows) {
+        CK(launch_k(true, b8::k_block8_claim, dim3(grid_for(n, 256, f.sms)), dim3(256), 0, st, slots, n, m->rows,
+                    m->claims));
+        claims = m->claims;
+    }
+    const bool cols = col_stride != 1;
+    const int64_t ldx = cols ? col_stride : row_stride;
+    const size_t esz = dtype_size(dtype);
+    const int per = cols ? 2 : 4;  // values per load
+    const int vec_ok = (uintptr_t)X % (per * esz) == 0 && ldx % per == 0;
+    const int64_t nb = b8_blocks(m->d);
+    const int grid = cols ? (int)std::min<int64_t>((n + b8::kColRows - 1) / b8::kColRows * nb, (int64_t)f.sms * 8)
+                          : grid_for((n * nb + 3) / 4 * 32, 256, f.sms, 8);
+    cudaError_t e;
+    switch (dtype) {
+        case EM_DTYPE_F32: e = b8_launch_write<float>(cols, grid, st, X, n, m->d, ldx, vec_ok, slots, first, claims, m); break;
+        case EM_DTYPE_BF16:
+            e = b8_launch_write<__nv_bfloat16>(cols, grid, st, X, n, m->d, ldx, vec_ok, slots, first, claims, m);
+            break;
+        default: e = b8_launch_write<__half>(cols, grid, st, X, n, m->d, ldx, vec_ok, slots, first, claims, m); break;
+    }
+    CK(e);
+    return EM_OK;
+}
+
+int em_block8_read(const em_block8_t* m, int64_t first, const int64_t* slots, int64_t n, void* out, int dtype,
+                   int64_t row_stride, void* stream) {
+    CKR(b8_check(m));
+    CKR(b8_check_dtype(dtype, out, "out"));
+    CKR(b8_check_rows(m, first, slots, n));
+    if (row_stride < m->d) return fail(EM_E_INVAL, "row_stride is below d");
+    if (n == 0) return EM_OK;
+    if (!out) return fail(EM_E_INVAL, "out is NULL");
+    const void* ptrs[] = {m->codes, m->scales, m->status, out, slots};
+    int dev;
+    CKR(same_device("em_block8_read", ptrs, 5, &dev));
+    DeviceGuard guard;
+    CK(guard.to(dev));
+    DeviceFacts f;
+    CKR(b8_device(dev, &f));
+    return b8_read(m, first, slots, n, out, dtype, row_stride, m->d, f.sms, static_cast<cudaStream_t>(stream));
+}
+
+int em_block8_matmul(const em_block8_t* a, int64_t na, const em_block8_t* b, int64_t nb, void* out, int dtype,
+                     int64_t row_stride, void* stream) {
+    CKR(b8_check(a));
+    CKR(b8_check(b));
+    CKR(b8_check_dtype(dtype, out, "out"));
+    if (a->d != b->d)
+        return fail(EM_E_INVAL, "the matrices have rows of %lld and %lld values", (long long)a->d, (long long)b->d);
+    if (na < 0 || na > a->rows || nb < 0 || nb > b->rows)
+        return fail(EM_E_INVAL, "na and nb must be within the matrices' rows");
+    if (row_stride < nb) return fail(EM_E_INVAL, "row_stride is below nb");
+    if (na == 0 || nb == 0) return EM_OK;
+    if (!out) return fail(EM_E_INVAL, "out is NULL");
+    const void* ptrs[] = {a->codes, a->scales, a->status, b->codes, b->scales, out};
+    int dev;
+    CKR(same_device("em_block8_matmul", ptrs, 6, &dev));
+    DeviceGuard guard;
+    CK(guard.to(dev));
+    DeviceFacts f;
+    CKR(b8_device(dev, &f));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    b8::MmArgs p = {};
+    p.out = out;
+    p.ldo = row_stride;
+    p.bf16 = dtype == EM_DTYPE_BF16;
+    p.wait_limit = 2000ll * f.clock_khz;
+    p.status = a->status;
+    const size_t esz = dtype_size(dtype);
+    p.vec_ok = (uintptr_t)out % 16 == 0 && row_stride * esz % 16 == 0;
+    if (na <= 128 && nb > na) {  // few output rows: the rows of b take the tiles' 128 lanes
+        p.m_rows = nb;
+        p.n_rows = na;
+        return esz == 4 ? b8_launch_matmul<128, 4, true>(b, a, p, f.sms, st)
+                        : b8_launch_matmul<128, 2, true>(b, a, p, f.sms, st);
+    }
+    p.m_rows = na;
+    p.n_rows = nb;
+    return esz == 4 ? b8_launch_matmul<128, 4, false>(a, b, p, f.sms, st)
+                    : b8_launch_matmul<128, 2, false>(a, b, p, f.sms, st);
+}
+
+int em_block8_check(const em_block8_t* m, void* stream) {
+    CKR(b8_check(m));
+    const void* ptrs[] = {m->status};
+    int dev;
+    CKR(same_device("em_block8_check", ptrs, 1, &dev));
+    DeviceGuard guard;
+    CK(guard.to(dev));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int32_t h = 0;
+    CK(cudaMemcpyAsync(&h, m->status, sizeof(h), cudaMemcpyDeviceToHost, st));
+    CK(cudaStreamSynchronize(st));
+    if (h != 0) {
+        CK(cudaMemsetAsync(m->status, 0, sizeof(h), st));
+        CK(cudaStreamSynchronize(st));
+        return fail(h, h == EM_E_TIMEOUT ? "a device-side wait exceeded its limit"
+                                         : "a slot is outside the matrix (device error %d)",
+                    (int)h);
+    }
+    return EM_OK;
+}
+
+}  // extern "C"

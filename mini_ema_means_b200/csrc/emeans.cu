@@ -47,6 +47,7 @@
 #include "k_reduce.cuh"
 #include "k_revive.cuh"
 #include "k_fp8.cuh"
+#include "k_block8.cuh"
 
 using namespace em;
 
@@ -490,11 +491,33 @@ static int grid_for(int64_t work, int block, int sms, int per_sm = 8) {
     return (int)std::max<int64_t>(g, 1);
 }
 
+static int read_block8(em_model* m, const em_block8_t* x, int64_t n, __nv_bfloat16* out);
+
+// EM_OPT_CHECK_FINITE: EM_E_NONFINITE if any of `count` values is NaN or infinite.
+static int check_finite(em_model* m, const void* src, int64_t count, bool bf16) {
+    CK(cudaMemsetAsync(m->flag.p, 0, sizeof(int), m->stream));
+    k_check_finite<<<grid_for(count, 256, m->sms), 256, 0, m->stream>>>(src, count, bf16, m->flag.p);
+    CK(cudaGetLastError());
+    int h = 0;
+    CK(cudaMemcpyAsync(&h, m->flag.p, sizeof(int), cudaMemcpyDeviceToHost, m->stream));
+    CK(cudaStreamSynchronize(m->stream));
+    if (h) return fail(EM_E_NONFINITE, "input holds NaN or infinite values");
+    return EM_OK;
+}
+
 // Makes a bf16 n x ld device copy of X (or uses X in place). *out receives the
 // row source the kernels read.
 static int prepare_input(em_model* m, const void* X, int64_t n, DBuf<__nv_bfloat16>& own,
                          const __nv_bfloat16** out) {
     if (!X || n < 1) return fail(EM_E_INVAL, "X is NULL or n < 1");
+    if (m->in_dtype == EM_DTYPE_BLOCK8) {
+        CKR(own.ensure((size_t)n * m->ld));
+        CKR(read_block8(m, static_cast<const em_block8_t*>(X), n, own.p));
+        EM_LAUNCHED(m, 1);
+        if (m->check_finite) CKR(check_finite(m, own.p, n * m->ld, true));
+        *out = own.p;
+        return EM_OK;
+    }
     const bool dev = is_device_ptr(X);
     const size_t esz = m->in_dtype == 1 ? 2 : 4;
     const size_t raw_bytes = (size_t)n * (size_t)m->d * esz;
@@ -504,16 +527,7 @@ static int prepare_input(em_model* m, const void* X, int64_t n, DBuf<__nv_bfloat
         CK(cudaMemcpyAsync(m->stage.p, X, raw_bytes, cudaMemcpyHostToDevice, m->stream));
         src = m->stage.p;
     }
-    if (m->check_finite) {
-        CK(cudaMemsetAsync(m->flag.p, 0, sizeof(int), m->stream));
-        k_check_finite<<<grid_for(n * m->d, 256, m->sms), 256, 0, m->stream>>>(src, n * m->d, m->in_dtype == 1,
-                                                                                m->flag.p);
-        CK(cudaGetLastError());
-        int h = 0;
-        CK(cudaMemcpyAsync(&h, m->flag.p, sizeof(int), cudaMemcpyDeviceToHost, m->stream));
-        CK(cudaStreamSynchronize(m->stream));
-        if (h) return fail(EM_E_NONFINITE, "input holds NaN or infinite values");
-    }
+    if (m->check_finite) CKR(check_finite(m, src, n * m->d, m->in_dtype == 1));
     if (m->in_dtype == 1 && m->ld == m->d && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
         *out = reinterpret_cast<const __nv_bfloat16*>(src);
         return EM_OK;
@@ -1552,7 +1566,8 @@ int em_set_option(em_model* m, int opt, double v) {
             m->law = (int)v;
             break;
         case EM_OPT_INPUT_DTYPE:
-            if (v != 0 && v != 1) return fail(EM_E_INVAL, "input dtype is 0 (fp32) or 1 (bf16)");
+            if (v != EM_DTYPE_F32 && v != EM_DTYPE_BF16 && v != EM_DTYPE_BLOCK8)
+                return fail(EM_E_INVAL, "input dtype is 0 (fp32), 1 (bf16) or 3 (block8)");
             m->in_dtype = (int)v;
             break;
         case EM_OPT_CHECK_FINITE: m->check_finite = v != 0; break;
@@ -2282,3 +2297,5 @@ extern "C" int em_assign_noalloc(const void* X, int64_t n, int64_t d, const floa
     if (h != 0) return fail(h, "device-side error %d in the assignment", h);
     return EM_OK;
 }
+
+#include "block8.cuh"

@@ -1,0 +1,701 @@
+// k_block8.cuh -- block-scaled E4M3 matrices: writing, reading back, products.
+//
+// A block8 matrix holds rows of d values as E4M3 codes with one power-of-two scale
+// per block of 128 values along the row. With a the largest magnitude among a
+// block's finite values, its exponent is
+//     e = the smallest integer with a <= 448 * 2^e, within [-117, 119]   (0 if a = 0)
+// and a value x is held as c = e4m3(x * 2^-e), nearest even, standing for c * 2^e.
+// The scaling is exact, so each value is rounded once; codes are floating point, so
+// a power of two costs them no relative accuracy (only up to one bit of the range
+// below the block's maximum). Four significant bits and a smallest value of
+// 2^-9 * 2^-117 = 2^-126 make every held value exact in fp32 and in bf16, and the
+// largest, 448 * 2^119 = 1.75 * 2^127, is finite there (fp32 values beyond it
+// saturate). NaN and infinities are held as NaN and leave their block's scale alone.
+//
+// Layout: codes are rows of round_up(d, 16) bytes (TMA wants 16-byte rows), zeros
+// past d. Exponents are bytes e + 127 (E8M0) in the order in which the tensor cores
+// take scale factors, so that a product copies them to tensor memory as they are:
+// [row / 128][block / 4][row % 32][(row / 32) % 4][block % 4], 512 bytes for each
+// 128 rows x 4 blocks (block8_scale_at).
+#pragma once
+
+#include "k_assign.cuh"
+#include "k_data.cuh"
+
+namespace em {
+namespace b8 {
+
+constexpr int kBlock = 128;       // values per scale
+constexpr int kMinExp = -117, kMaxExp = 119;
+constexpr int kAtomBytes = 512;   // exponents of 128 rows x 4 blocks
+
+__host__ __device__ __forceinline__ int64_t scale_at(int64_t row, int64_t block, int64_t groups) {
+    return ((((row >> 7) * groups + (block >> 2)) * 32 + (row & 31)) * 4 + ((row >> 5) & 3)) * 4 + (block & 3);
+}
+
+// The exponent of a block from the bit pattern of its largest finite magnitude:
+// 448 = 1.75 * 2^8, so e is the magnitude's own exponent less 8, one more where its
+// mantissa is above 1.75.
+__device__ __forceinline__ int block_exponent(uint32_t amax_bits) {
+    const int e = (int)(amax_bits >> 23) - 135 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return amax_bits == 0u ? 0 : min(max(e, kMinExp), kMaxExp);
+}
+
+// |x| as an order-preserving integer, 0 for NaN and infinities.
+__device__ __forceinline__ uint32_t finite_magnitude(float x) {
+    const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+    return b < 0x7F800000u ? b : 0u;
+}
+
+// Two E4M3 codes (lo in the low byte) of values already scaled; infinities become NaN
+// as NaN does (the conversion alone would saturate them).
+__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+    uint16_t r;
+    lo = finite_magnitude(lo) == 0u && lo != 0.0f ? __int_as_float(0x7FC00000) : lo;
+    hi = finite_magnitude(hi) == 0u && hi != 0.0f ? __int_as_float(0x7FC00000) : hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t encode4(const float v[4], float inverse) {
+    return encode2(v[0] * inverse, v[1] * inverse) | (encode2(v[2] * inverse, v[3] * inverse) << 16);
+}
+
+__device__ __forceinline__ void decode4(uint32_t codes, float v[4]) {
+    uint32_t h0, h1;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h0) : "h"((uint16_t)(codes & 0xFFFFu)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h1) : "h"((uint16_t)(codes >> 16)));
+    __half2 a, b;
+    memcpy(&a, &h0, 4);
+    memcpy(&b, &h1, 4);
+    const float2 fa = __half22float2(a), fb = __half22float2(b);
+    v[0] = fa.x; v[1] = fa.y; v[2] = fb.x; v[3] = fb.y;
+}
+
+// 2^e of an exponent byte as a float (bytes 10..246 are written; 0 would be a
+// subnormal and reads as 0).
+__device__ __forceinline__ float scale_of(uint8_t byte) { return __uint_as_float((uint32_t)byte << 23); }
+
+template <class T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <class T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
+
+template <class T>
+struct alignas(4 * sizeof(T)) Vec4 { T v[4]; };
+
+// Where row i of a call goes (write) or comes from (read): row first + i, or slots[i].
+// Returns -1 for a row to leave out: slot -1 (padding), or a slot outside the matrix,
+// which also raises EM_E_BOUNDS.
+__device__ __forceinline__ int64_t slot_of(const int64_t* __restrict__ slots, int64_t first, int64_t i, int64_t rows,
+                                           int* status) {
+    if (!slots) return first + i;
+    const int64_t s = slots[i];
+    if (s >= 0 && s < rows) return s;
+    if (s != -1) raise_error(status, EM_E_BOUNDS);
+    return -1;
+}
+
+// Several rows of one call may name the same slot: the last of them stays, whole.
+// Calls of up to kScanRows rows look for a later row with the same slot where they
+// write; longer calls run this pass first, which leaves in claims[slot] the last row
+// of this call that names it. An entry from an earlier call counts only if that row
+// of this call names the slot too, so the array needs no initial value, and a
+// captured call can be replayed at any time. The loop ends: an entry is replaced by a
+// valid one or by a later row, at most once for each row that names the slot.
+constexpr int kScanRows = 512;
+
+__global__ void k_block8_claim(const int64_t* __restrict__ slots, int64_t n, int64_t rows, int* __restrict__ claims) {
+    pdl_wait();
+    pdl_release();
+    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t s = slots[i];
+        if (s < 0 || s >= rows) continue;
+        int cur = *(volatile int*)(claims + s);
+        for (;;) {
+            const bool valid = cur >= 0 && cur < n && slots[cur] == s;
+            if (valid && cur >= (int)i) break;
+            const int seen = atomicCAS(claims + s, cur, (int)i);
+            if (seen == cur) break;
+            cur = seen;
+        }
+    }
+}
+
+// Whether row i is the one that stays in its slot s. Takes the whole warp.
+__device__ __forceinline__ bool last_of_slot(const int64_t* __restrict__ slots, const int* __restrict__ claims,
+                                             int64_t i, int64_t n, int64_t s, int lane) {
+    if (!slots || s < 0) return true;
+    if (claims) return claims[s] == (int)i;
+    bool later = false;
+    for (int64_t j = i + 1 + lane; j < n; j += 32) later |= slots[j] == s;
+    return !__any_sync(0xFFFFFFFFu, later);
+}
+
+// Writes rows (values of a row contiguous, rows `ldx` apart). One warp takes four
+// consecutive (row, block) pairs at a time, 4 values of each block per lane: four
+// independent loads in flight per lane at every width (a row of 96 values alone is
+// one block), one redux.sync for a block's maximum, 128 bytes of codes per store.
+template <class T>
+__global__ void __launch_bounds__(256)
+    k_block8_write(const T* __restrict__ X, int64_t n, int64_t d, int64_t ldx, int vec_ok,
+                   const int64_t* __restrict__ slots, int64_t first, const int* __restrict__ claims,
+                   uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t rows, int64_t pitch, int* status) {
+    pdl_wait();
+    pdl_release();
+    const int lane = threadIdx.x & 31;
+    const int64_t warp = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
+    const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+    const int64_t nb = (d + kBlock - 1) / kBlock, groups = (nb + 3) / 4, total = n * nb;
+    for (int64_t f0 = warp * 4; f0 < total; f0 += nwarps * 4) {
+        int64_t row = total <= 0xFFFFFFFFll ? (int64_t)((uint32_t)f0 / (uint32_t)nb) : f0 / nb;
+        int64_t b = f0 - row * nb;
+        float v[4][4];
+        int64_t rr[4], bb[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            rr[s] = f0 + s < total ? row : -1;
+            bb[s] = b;
+            if (++b == nb) {
+                b = 0;
+                ++row;
+            }
+            const int64_t col = bb[s] * kBlock + 4 * lane;
+            const T* src = X + rr[s] * ldx + col;
+            if (rr[s] >= 0 && vec_ok && col + 4 <= d) {
+                const Vec4<T> x = *reinterpret_cast<const Vec4<T>*>(src);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) v[s][t] = to_f32(x.v[t]);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) v[s][t] = rr[s] >= 0 && col + t < d ? to_f32(src[t]) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (rr[s] < 0) break;
+            const int64_t to = slot_of(slots, first, rr[s], rows, status);
+            if (to < 0 || !last_of_slot(slots, claims, rr[s], n, to, lane)) continue;
+            uint32_t a = 0u;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) a = max(a, finite_magnitude(v[s][t]));
+            const int e = block_exponent(__reduce_max_sync(0xFFFFFFFFu, a));
+            const float inverse = __uint_as_float((uint32_t)(127 - e) << 23);
+            const int64_t col = bb[s] * kBlock + 4 * lane;
+            if (col < pitch) *reinterpret_cast<uint32_t*>(codes + to * pitch + col) = encode4(v[s], inverse);
+            if (lane == 0) scales[scale_at(to, bb[s], groups)] = (uint8_t)(e + 127);
+        }
+    }
+}
+
+// Writes rows given as columns: value j of row i is X[j * ldx + i], so consecutive
+// rows are contiguous in memory. A block of 256 threads takes 64 rows x one block of
+// 128 values: warp w loads values 16 w .. 16 w + 15, two rows per lane, and keeps
+// them in registers; the rows' maxima meet in shared memory; the codes are turned in
+// shared memory and leave as 128 bytes per row.
+constexpr int kColRows = 64;
+
+template <class T>
+struct alignas(2 * sizeof(T)) Vec2 { T v[2]; };
+
+template <class T>
+__global__ void __launch_bounds__(256)
+    k_block8_write_cols(const T* __restrict__ X, int64_t n, int64_t d, int64_t ldx, int vec_ok,
+                        const int64_t* __restrict__ slots, int64_t first, const int* __restrict__ claims,
+                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t rows, int64_t pitch,
+                        int* status) {
+    constexpr int kPitch = kBlock + 4;
+    __shared__ uint32_t amax[8][kColRows];
+    __shared__ __align__(16) uint8_t turned[kColRows * kPitch];
+    pdl_wait();
+    pdl_release();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t nb = (d + kBlock - 1) / kBlock, groups = (nb + 3) / 4;
+    const int64_t row_tiles = (n + kColRows - 1) / kColRows;
+    for (int64_t t = blockIdx.x; t < row_tiles * nb; t += gridDim.x) {
+        const int64_t b = t / row_tiles, i0 = (t - b * row_tiles) * kColRows + 2 * lane;
+        float v[2][16];
+        uint32_t a[2] = {0u, 0u};
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const int64_t j = b * kBlock + 16 * w + k;
+            const T* src = X + j * ldx + i0;
+            v[0][k] = v[1][k] = 0.0f;
+            if (j < d) {
+                if (vec_ok && i0 + 2 <= n) {
+                    const Vec2<T> x = *reinterpret_cast<const Vec2<T>*>(src);
+                    v[0][k] = to_f32(x.v[0]);
+                    v[1][k] = to_f32(x.v[1]);
+                } else {
+                    if (i0 < n) v[0][k] = to_f32(src[0]);
+                    if (i0 + 1 < n) v[1][k] = to_f32(src[1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            a[0] = max(a[0], finite_magnitude(v[0][k]));
+            a[1] = max(a[1], finite_magnitude(v[1][k]));
+        }
+        amax[w][2 * lane] = a[0];
+        amax[w][2 * lane + 1] = a[1];
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            uint32_t m = 0u;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m = max(m, amax[q][2 * lane + r]);
+            const int e = block_exponent(m);
+            const float inverse = __uint_as_float((uint32_t)(127 - e) << 23);
+            uint32_t* dst = reinterpret_cast<uint32_t*>(turned + (2 * lane + r) * kPitch + 16 * w);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) dst[q] = encode4(&v[r][4 * q], inverse);
+        }
+        __syncthreads();
+        // 8 rows per warp, 4 codes per lane
+        for (int r = 0; r < kColRows / 8; ++r) {
+            const int rl = w * (kColRows / 8) + r;
+            const int64_t i = (t - b * row_tiles) * kColRows + rl;
+            if (i >= n) break;
+            const int64_t to = slot_of(slots, first, i, rows, status);
+            if (to < 0 || !last_of_slot(slots, claims, i, n, to, lane)) continue;
+            const int64_t col = b * kBlock + 4 * lane;
+            if (col < pitch)
+                *reinterpret_cast<uint32_t*>(codes + to * pitch + col) =
+                    *reinterpret_cast<const uint32_t*>(turned + rl * kPitch + 4 * lane);
+            if (lane == 0) {
+                uint32_t m = 0u;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) m = max(m, amax[q][rl]);
+                scales[scale_at(to, b, groups)] = (uint8_t)(block_exponent(m) + 127);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Reads rows back, four (row, block) pairs per warp at a time as k_block8_write takes
+// them. Exact in fp32 and bf16; fp16 rounds to nearest even (and overflows to
+// infinity). Padding rows (slot -1) and rows outside the matrix read as zeros.
+// `ldo` columns are written for each row from d on up to `width` (zeros past d).
+template <class T>
+__global__ void __launch_bounds__(256)
+    k_block8_read(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int64_t pitch,
+                  int64_t d, const int64_t* __restrict__ slots, int64_t first, int64_t n, T* __restrict__ out,
+                  int64_t ldo, int64_t width, int vec_ok, int* status) {
+    pdl_wait();
+    pdl_release();
+    const int lane = threadIdx.x & 31;
+    const int64_t warp = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
+    const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+    const int64_t nb = (d + kBlock - 1) / kBlock, groups = (nb + 3) / 4, total = n * nb;
+    for (int64_t f0 = warp * 4; f0 < total; f0 += nwarps * 4) {
+        int64_t row = total <= 0xFFFFFFFFll ? (int64_t)((uint32_t)f0 / (uint32_t)nb) : f0 / nb;
+        int64_t b = f0 - row * nb;
+        uint32_t c[4];
+        float sc[4];
+        int64_t rr[4], bb[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            rr[s] = f0 + s < total ? row : -1;
+            bb[s] = b;
+            if (++b == nb) {
+                b = 0;
+                ++row;
+            }
+            c[s] = 0u;
+            sc[s] = 0.0f;
+            if (rr[s] >= 0) {
+                const int64_t from = slot_of(slots, first, rr[s], rows, status);
+                const int64_t col = bb[s] * kBlock + 4 * lane;
+                if (from >= 0) {
+                    if (col < pitch) c[s] = *reinterpret_cast<const uint32_t*>(codes + from * pitch + col);
+                    sc[s] = scale_of(scales[scale_at(from, bb[s], groups)]);
+                }
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (rr[s] < 0) break;
+            float v[4];
+            decode4(c[s], v);
+            const int64_t col = bb[s] * kBlock + 4 * lane;
+            T* dst = out + rr[s] * ldo + col;
+            Vec4<T> o;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) o.v[t] = from_f32<T>(col + t < d ? v[t] * sc[s] : 0.0f);
+            if (vec_ok && col + 4 <= width) {
+                *reinterpret_cast<Vec4<T>*>(dst) = o;
+            } else {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    if (col + t < width) dst[t] = o.v[t];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- product
+//
+// out = A B^T of two block8 matrices on the tensor cores' block-scaled FP8 path
+// (tcgen05.mma kind::mxf8f6f4, fp32 accumulators): the scales enter the MMA as E8M0
+// factors, so a product of held values is exact and only the accumulation rounds.
+// The hardware takes one factor per 32 values of a row; the four K = 32 steps of a
+// block name the same byte (the scale-factor id of the instruction descriptor picks
+// byte block % 4 of the row's word), so one stored byte serves 128 values.
+//
+// One CTA per SM, persistent over output tiles of 128 x BN:
+//   warp 0     one thread loads 128 x 128 codes of A, BN x 128 of B (TMA, 128-byte
+//              swizzle) and the exponents of their rows into a ring of stages
+//   warp 1     one thread copies a stage's exponents to tensor memory (each stage has
+//              its own columns there, so a copy never meets an MMA that still reads
+//              the last ones) and issues the MMAs into one of two accumulators
+//   warps 2-9  epilogue: two groups of four warps (one per TMEM lane quadrant) take
+//              the left and right half of a tile's columns
+// SWAP: A is the operand whose rows are the output's columns (few output rows): a
+// lane then holds one output column and a warp stores 32 neighbours at once.
+// Otherwise a warp turns 32 rows x 128 bytes in shared memory and stores whole
+// 128-byte row pieces.
+
+// Waits for a phase of `bar`; after `limit` clock cycles it raises EM_E_TIMEOUT and the
+// CTA's abort flag and gives up. (An error that an earlier call left in the matrix's
+// status word, an out-of-range slot say, does not stop a product: only this CTA's own
+// waits do.)
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, long long limit, int* status,
+                                         volatile int* abort_flag) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t it = 1;; ++it) {
+        if (tc::mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort_flag) return false;
+            if (clock64() - t0 > limit) {
+                raise_error(status, EM_E_TIMEOUT);
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
+
+constexpr int kMmThreads = 320;
+constexpr int kMmEpi = 256;
+
+template <int BN>
+struct MmCfg {
+    static constexpr int kABytes = 128 * 128;
+    static constexpr int kBBytes = BN * 128;
+    static constexpr int kBAtoms = (BN + 127) / 128;
+    static constexpr int kSfBytes = (1 + kBAtoms) * kAtomBytes;
+    static constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
+    static constexpr int kTurnBytes = 8 * 32 * 128;  // epilogue warps' turning buffers
+    static constexpr int kFixed = 1024 + 256 + kTurnBytes;
+    static constexpr int kStages = (227 * 1024 - kFixed) / kStageBytes > 8 ? 8 : (227 * 1024 - kFixed) / kStageBytes;
+    static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
+    static constexpr int kSfCols = 4 * (1 + kBAtoms);  // tensor-memory columns of a stage's exponents
+    static constexpr int kSfBase = 2 * BN;
+    static_assert(kSfBase + kStages * kSfCols <= 512, "tensor memory");
+};
+
+// Instruction descriptor of tcgen05.mma kind::mxf8f6f4: the scale-factor ids in bits
+// 4-5 (B) and 29-30 (A), E4M3 operands (format 0 in bits 7-9 and 10-12), K-major (bits
+// 15, 16 = 0), N >> 3 in bits 17-22, E8M0 scales (bit 23), M >> 7 in bits 27-28.
+__device__ __forceinline__ uint32_t mm_idesc(int n, uint32_t sf_id) {
+    return (sf_id << 4) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | (1u << 27) | (sf_id << 29);
+}
+
+__device__ __forceinline__ void umma_block8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                            uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// 512 bytes of exponents to four tensor-memory columns, repeated in each lane
+// quadrant. The descriptor: no swizzle, 8-row groups of 16-byte rows 128 bytes apart.
+__device__ __forceinline__ void copy_exponents(uint32_t tmem, uint32_t smem) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(tc::smem_desc(smem, 0ull, 128u))
+                 : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+struct MmArgs {
+    const uint8_t* sfa;   // exponents of the M operand, of the N operand
+    const uint8_t* sfb;
+    void* out;
+    int64_t ldo;
+    int64_t m_rows, n_rows;  // rows of the M and N operands that the product takes
+    int64_t n_atoms;         // 128-row groups of the N operand's matrix
+    int nkb;                 // blocks along the rows
+    int m_tiles, n_tiles;
+    int bf16;                // 16-bit results: bf16 rather than fp16
+    int vec_ok;              // 16-byte aligned output rows
+    long long wait_limit;
+    int* status;
+};
+
+// 32 fp32 accumulators of a lane as 32 / CPW output words (CPW = columns per word).
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi, int bf16) {
+    uint32_t r;
+    if (bf16) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+        memcpy(&r, &p, 4);
+    } else {
+        const __half2 p = __floats2half2_rn(lo, hi);
+        memcpy(&r, &p, 4);
+    }
+    return r;
+}
+
+template <int BN, int OB, bool SWAP>
+__global__ void __launch_bounds__(kMmThreads, 1)
+    k_block8_matmul(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const MmArgs p) {
+    using C = MmCfg<BN>;
+    using namespace tc;
+    constexpr int S = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = sA + S * C::kABytes;
+    uint8_t* turn = sB + S * C::kBBytes;  // 128-byte aligned rows
+    uint8_t* sSf = turn + C::kTurnBytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sSf + S * C::kSfBytes);
+    uint64_t* full = bars;
+    uint64_t* empty = bars + S;
+    uint64_t* tfull = bars + 2 * S;
+    uint64_t* tempty = bars + 2 * S + 2;
+    uint64_t* drain = bars + 2 * S + 4;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long drain_limit = p.wait_limit > 4000000000ll ? p.wait_limit : 4000000000ll;
+    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+    const int groups = (p.nkb + 3) / 4;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&tfull[a]), 1);
+            mbar_init(smem_u32(&tempty[a]), kMmEpi);
+        }
+        mbar_init(smem_u32(drain), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (warp == 0 && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmA) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmB) : "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();
+    pdl_release();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, armed = 0, armed_parity = 0;
+            bool ok = true;
+            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
+                const int64_t atom_b = (int64_t)n * BN / 128;
+                const int atoms_b = (int)min((int64_t)C::kBAtoms, p.n_atoms - atom_b);
+                for (int kb = 0; kb < p.nkb; ++kb) {
+                    if (!wait_bar(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&full[stage]);
+                    armed |= 1u << stage;
+                    armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                    mbar_expect_tx(fb, (uint32_t)(C::kABytes + C::kBBytes + (1 + atoms_b) * kAtomBytes));
+                    tma_load_2d(smem_u32(sA + stage * C::kABytes), &tmA, kb * kBlock, m * 128, fb);
+                    tma_load_2d(smem_u32(sB + stage * C::kBBytes), &tmB, kb * kBlock, n * BN, fb);
+                    uint8_t* sf = sSf + stage * C::kSfBytes;
+                    bulk_load(smem_u32(sf), p.sfa + ((int64_t)m * groups + (kb >> 2)) * kAtomBytes, kAtomBytes, fb);
+                    for (int q = 0; q < atoms_b; ++q)
+                        bulk_load(smem_u32(sf + (1 + q) * kAtomBytes),
+                                  p.sfb + ((atom_b + q) * groups + (kb >> 2)) * kAtomBytes, kAtomBytes, fb);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok)
+                for (int s = 0; s < S; ++s)
+                    if (armed & (1u << s)) mbar_drain(smem_u32(&full[s]), (armed_parity >> s) & 1u, drain_limit);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                if (!wait_bar(smem_u32(&tempty[acc]), acc_phase ^ 1u, p.wait_limit, p.status, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+                for (int kb = 0; kb < p.nkb; ++kb) {
+                    if (!wait_bar(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sf = tmem_base + (uint32_t)(C::kSfBase + stage * C::kSfCols);
+                    const uint32_t ssf = smem_u32(sSf + stage * C::kSfBytes);
+#pragma unroll
+                    for (int q = 0; q < 1 + C::kBAtoms; ++q) copy_exponents(sf + 4 * q, ssf + q * kAtomBytes);
+                    const uint32_t a0 = smem_u32(sA + stage * C::kABytes), b0 = smem_u32(sB + stage * C::kBBytes);
+                    const uint32_t idesc = mm_idesc(BN, (uint32_t)(kb & 3));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_block8(d_tmem, smem_desc(a0 + kk * 32, 2ull, 1024u), smem_desc(b0 + kk * 32, 2ull, 1024u),
+                                    idesc, sf, sf + 4, (kb | kk) != 0);
+                    umma_commit(smem_u32(&empty[stage]));
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                umma_commit(smem_u32(&tfull[acc]));
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            if (!ok) {
+                umma_commit(smem_u32(drain));
+                mbar_drain(smem_u32(drain), 0u, drain_limit);
+            }
+        }
+    } else {
+        const int ew = warp - 2;
+        const int q = warp & 3, half = ew >> 2;
+        const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+        uint8_t* buf = turn + ew * 32 * 128;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+            const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
+            if (!__all_sync(0xFFFFFFFFu,
+                            wait_bar(smem_u32(&tfull[acc]), acc_phase, p.wait_limit, p.status, abort_flag)))
+                break;
+            tc_fence_after();
+            const uint32_t tbase = tmem_base + lane_base + (uint32_t)(acc * BN + half * (BN / 2));
+            const int64_t row0 = (int64_t)m * 128 + 32 * q;
+            const int64_t col0 = (int64_t)n * BN + half * (BN / 2);
+            constexpr int kChunk = OB == 4 || SWAP ? 32 : 64;  // columns: 128 bytes of output row
+#pragma unroll
+            for (int c = 0; c < BN / 2; c += kChunk) {
+                uint32_t w[32];
+                if (kChunk == 32) {
+                    tmem_ld32(tbase + c, w);
+                    tmem_wait_ld32(w);
+                } else {
+                    uint32_t u[32];
+                    tmem_ld32(tbase + c, u);
+                    tmem_wait_ld32(u);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        w[i] = pack_out(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]), p.bf16);
+                    tmem_ld32(tbase + c + 32, u);
+                    tmem_wait_ld32(u);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        w[16 + i] = pack_out(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]), p.bf16);
+                }
+                if (c + kChunk >= BN / 2) {  // the tile's last load is in registers
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&tempty[acc]));
+                }
+                if (SWAP) {
+                    const int64_t j = row0 + lane;  // output column
+                    if (j < p.m_rows) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int64_t r = col0 + c + i;  // output row
+                            if (r < p.n_rows) {
+                                if (OB == 4)
+                                    reinterpret_cast<uint32_t*>(p.out)[r * p.ldo + j] = w[i];
+                                else
+                                    reinterpret_cast<uint16_t*>(p.out)[r * p.ldo + j] =
+                                        (uint16_t)pack_out(__uint_as_float(w[i]), 0.0f, p.bf16);
+                            }
+                        }
+                    }
+                } else {
+                    if (col0 + c >= p.n_rows) continue;
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    __syncwarp();
+                    const int64_t cc = col0 + c + (lane & 7) * (16 / OB);  // this lane's first column
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + (lane >> 3);
+                        const uint4 x = *reinterpret_cast<const uint4*>(buf + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                        if (row0 + r < p.m_rows) {
+                            uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + ((row0 + r) * p.ldo + cc) * OB;
+                            if (p.vec_ok && cc + 16 / OB <= p.n_rows) {
+                                *reinterpret_cast<uint4*>(dst) = x;
+                            } else {
+                                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int e = 0; e < 16 / OB; ++e)
+                                    if (cc + e < p.n_rows) {
+                                        if (OB == 4)
+                                            reinterpret_cast<uint32_t*>(dst)[e] = xs[e];
+                                        else
+                                            reinterpret_cast<uint16_t*>(dst)[e] =
+                                                (uint16_t)(xs[e >> 1] >> (16 * (e & 1)));
+                                    }
+                            }
+                        }
+                    }
+                }
+            }
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u) : "memory");
+    }
+}
+
+}  // namespace b8
+}  // namespace em
