@@ -79,7 +79,9 @@ int b8_check_dtype(int dtype, const void* p, const char* what) {
 
 // Rows [first, first + n) or slots; n within the limits of the row indexes.
 int b8_check_rows(const em_block8_t* m, int64_t first, const int64_t* slots, int64_t n) {
-    if (n < 0 || n >= (1ll << 31)) return fail(EM_E_INVAL, "need 0 <= n < 2^31 (n = %lld)", (long long)n);
+    // (the kernels count (row, block) pairs in 31 bits; 2^31 pairs are 270 GB of codes)
+    if (n < 0 || n >= (1ll << 31) || n * b8_blocks(m->d) >= (1ll << 31))
+        return fail(EM_E_INVAL, "need 0 <= n and n x ceil(d / 128) < 2^31 (n = %lld)", (long long)n);
     if (slots) {
         if (first != 0) return fail(EM_E_INVAL, "first must be 0 with slots");
         if ((uintptr_t)slots & 7) return fail(EM_E_INVAL, "slots must be 8-byte aligned");
@@ -127,36 +129,51 @@ int b8_device(int dev, DeviceFacts* out) {
     return EM_OK;
 }
 
-template <class T>
-cudaError_t b8_launch_write(bool cols, int grid, cudaStream_t st, const void* X, int64_t n, int64_t d, int64_t ldx,
-                            int vec_ok, const int64_t* slots, int64_t first, const int* claims, const em_block8_t* m) {
-    return launch_k(true, cols ? b8::k_block8_write_cols<T> : b8::k_block8_write<T>, dim3(grid), dim3(256), 0, st,
-                    static_cast<const T*>(X), n, d, ldx, vec_ok, slots, first, claims, static_cast<uint8_t*>(m->codes),
-                    static_cast<uint8_t*>(m->scales), m->rows, b8_pitch(d), m->status);
+int b8_pair_grid(int64_t n, int64_t nb, int sms) {
+    return grid_for((n * nb + b8::kPairsPerWarp - 1) / b8::kPairsPerWarp * 32, 256, sms, 8);
 }
 
 template <class T>
-cudaError_t b8_launch_read(int grid, cudaStream_t st, const em_block8_t* m, const int64_t* slots, int64_t first,
-                           int64_t n, void* out, int64_t ldo, int64_t width, int vec_ok) {
-    return launch_k(true, b8::k_block8_read<T>, dim3(grid), dim3(256), 0, st,
-                    static_cast<const uint8_t*>(m->codes), static_cast<const uint8_t*>(m->scales), m->rows,
-                    b8_pitch(m->d), m->d, slots, first, n, static_cast<T*>(out), ldo, width, vec_ok, m->status);
-}
-
-// Reads rows with no checks but the kernel's own (`width` columns per row).
-int b8_read(const em_block8_t* m, int64_t first, const int64_t* slots, int64_t n, void* out, int dtype, int64_t ldo,
-            int64_t width, int sms, cudaStream_t st) {
-    const int64_t pairs = n * b8_blocks(m->d);
-    const int grid = grid_for((pairs + 3) / 4 * 32, 256, sms, 8);
-    const int vec_ok = (uintptr_t)out % (4 * dtype_size(dtype)) == 0 && ldo % 4 == 0;
-    switch (dtype) {
-        case EM_DTYPE_F32: CK(b8_launch_read<float>(grid, st, m, slots, first, n, out, ldo, width, vec_ok)); break;
-        case EM_DTYPE_BF16:
-            CK(b8_launch_read<__nv_bfloat16>(grid, st, m, slots, first, n, out, ldo, width, vec_ok));
-            break;
-        default: CK(b8_launch_read<__half>(grid, st, m, slots, first, n, out, ldo, width, vec_ok)); break;
+int b8_write(bool cols, const void* X_, int64_t n, int64_t ldx, const int64_t* slots, int64_t first, const int* claims,
+             const em_block8_t* m, int sms, cudaStream_t st) {
+    const T* X = static_cast<const T*>(X_);
+    uint8_t* codes = static_cast<uint8_t*>(m->codes);
+    uint8_t* scales = static_cast<uint8_t*>(m->scales);
+    const int64_t nb = b8_blocks(m->d);
+    const int d = (int)m->d, pitch = (int)b8_pitch(m->d);
+    if (!cols) {
+        CK(launch_k(true, b8::k_block8_write<T>, dim3(b8_pair_grid(n, nb, sms)), dim3(256), 0, st, X, (int)n, d, ldx,
+                    b8::vector_width<T>(X, ldx), slots, first, claims, codes, scales, m->rows, pitch,
+                    b8::FastDiv((uint32_t)nb), m->status));
+        return EM_OK;
     }
+    const int64_t row_tiles = (n + b8::kColRows - 1) / b8::kColRows;
+    const int vec_ok = (uintptr_t)X % (2 * sizeof(T)) == 0 && ldx % 2 == 0;
+    const int grid = (int)std::min<int64_t>(row_tiles * nb, (int64_t)sms * 8);
+    CK(launch_k(true, b8::k_block8_write_cols<T>, dim3(grid), dim3(256), 0, st, X, (int)n, d, ldx, vec_ok, slots, first,
+                claims, codes, scales, m->rows, pitch, b8::FastDiv((uint32_t)row_tiles), m->status));
     return EM_OK;
+}
+
+template <class T>
+int b8_read_as(const em_block8_t* m, int64_t first, const int64_t* slots, int64_t n, void* out, int64_t ldo,
+               int64_t columns, int sms, cudaStream_t st) {
+    const int64_t nb = b8_blocks(m->d);
+    CK(launch_k(true, b8::k_block8_read<T>, dim3(b8_pair_grid(n, nb, sms)), dim3(256), 0, st,
+                static_cast<const uint8_t*>(m->codes), static_cast<const uint8_t*>(m->scales), m->rows,
+                (int)b8_pitch(m->d), (int)m->d, slots, first, (int)n, static_cast<T*>(out), ldo, (int)columns,
+                b8::vector_width<T>(out, ldo), b8::FastDiv((uint32_t)nb), m->status));
+    return EM_OK;
+}
+
+// Reads rows with no checks but the kernel's own (`columns` values per row, zeros past d).
+int b8_read(const em_block8_t* m, int64_t first, const int64_t* slots, int64_t n, void* out, int dtype, int64_t ldo,
+            int64_t columns, int sms, cudaStream_t st) {
+    switch (dtype) {
+        case EM_DTYPE_F32: return b8_read_as<float>(m, first, slots, n, out, ldo, columns, sms, st);
+        case EM_DTYPE_BF16: return b8_read_as<__nv_bfloat16>(m, first, slots, n, out, ldo, columns, sms, st);
+        default: return b8_read_as<__half>(m, first, slots, n, out, ldo, columns, sms, st);
+    }
 }
 
 }  // namespace
@@ -232,22 +249,11 @@ int em_block8_write(const em_block8_t* m, const void* X, int dtype, int64_t n, i
     }
     const bool cols = col_stride != 1;
     const int64_t ldx = cols ? col_stride : row_stride;
-    const size_t esz = dtype_size(dtype);
-    const int per = cols ? 2 : 4;  // values per load
-    const int vec_ok = (uintptr_t)X % (per * esz) == 0 && ldx % per == 0;
-    const int64_t nb = b8_blocks(m->d);
-    const int grid = cols ? (int)std::min<int64_t>((n + b8::kColRows - 1) / b8::kColRows * nb, (int64_t)f.sms * 8)
-                          : grid_for((n * nb + 3) / 4 * 32, 256, f.sms, 8);
-    cudaError_t e;
     switch (dtype) {
-        case EM_DTYPE_F32: e = b8_launch_write<float>(cols, grid, st, X, n, m->d, ldx, vec_ok, slots, first, claims, m); break;
-        case EM_DTYPE_BF16:
-            e = b8_launch_write<__nv_bfloat16>(cols, grid, st, X, n, m->d, ldx, vec_ok, slots, first, claims, m);
-            break;
-        default: e = b8_launch_write<__half>(cols, grid, st, X, n, m->d, ldx, vec_ok, slots, first, claims, m); break;
+        case EM_DTYPE_F32: return b8_write<float>(cols, X, n, ldx, slots, first, claims, m, f.sms, st);
+        case EM_DTYPE_BF16: return b8_write<__nv_bfloat16>(cols, X, n, ldx, slots, first, claims, m, f.sms, st);
+        default: return b8_write<__half>(cols, X, n, ldx, slots, first, claims, m, f.sms, st);
     }
-    CK(e);
-    return EM_OK;
 }
 
 int em_block8_read(const em_block8_t* m, int64_t first, const int64_t* slots, int64_t n, void* out, int dtype,

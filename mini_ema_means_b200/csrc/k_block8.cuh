@@ -41,24 +41,18 @@ __device__ __forceinline__ int block_exponent(uint32_t amax_bits) {
     return amax_bits == 0u ? 0 : min(max(e, kMinExp), kMaxExp);
 }
 
-// |x| as an order-preserving integer, 0 for NaN and infinities.
-__device__ __forceinline__ uint32_t finite_magnitude(float x) {
-    const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
-    return b < 0x7F800000u ? b : 0u;
+// NaN for NaN and infinities, x otherwise.
+__device__ __forceinline__ float finite_or_nan(float x) {
+    return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : x;
 }
 
-// Two E4M3 codes (lo in the low byte) of values already scaled; infinities become NaN
-// as NaN does (the conversion alone would saturate them).
-__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
-    uint16_t r;
-    lo = finite_magnitude(lo) == 0u && lo != 0.0f ? __int_as_float(0x7FC00000) : lo;
-    hi = finite_magnitude(hi) == 0u && hi != 0.0f ? __int_as_float(0x7FC00000) : hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
+// Codes of 4 scaled values (the first in the low byte). Infinities must have been made
+// NaN before: the conversion would saturate them.
 __device__ __forceinline__ uint32_t encode4(const float v[4], float inverse) {
-    return encode2(v[0] * inverse, v[1] * inverse) | (encode2(v[2] * inverse, v[3] * inverse) << 16);
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1] * inverse), "f"(v[0] * inverse));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3] * inverse), "f"(v[2] * inverse));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
 __device__ __forceinline__ void decode4(uint32_t codes, float v[4]) {
@@ -85,8 +79,81 @@ template <> __device__ __forceinline__ float from_f32(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
 
+template <class T, int N>
+struct alignas(N * sizeof(T)) Vec { T v[N]; };
+
+// The widest access, in elements, that rows at `base` with `ld` elements between them
+// allow: 16 bytes, 8 bytes, or single elements.
 template <class T>
-struct alignas(4 * sizeof(T)) Vec4 { T v[4]; };
+__host__ __device__ __forceinline__ int vector_width(const void* base, int64_t ld) {
+    for (int w = 16 / (int)sizeof(T); w >= 8 / (int)sizeof(T); w >>= 1)
+        if (reinterpret_cast<uintptr_t>(base) % (w * sizeof(T)) == 0 && ld % w == 0) return w;
+    return 1;
+}
+
+template <class T, int W>
+__device__ __forceinline__ void load8_as(const T* p, float v[8]) {
+#pragma unroll
+    for (int q = 0; q < 8 / W; ++q) {
+        const Vec<T, W> x = reinterpret_cast<const Vec<T, W>*>(p)[q];
+#pragma unroll
+        for (int t = 0; t < W; ++t) v[q * W + t] = to_f32(x.v[t]);
+    }
+}
+
+// 8 values from p, of which `left` exist (zeros after them).
+template <class T>
+__device__ __forceinline__ void load8(const T* p, int left, int width, float v[8]) {
+    if (left >= 8 && width == 16 / (int)sizeof(T)) {
+        load8_as<T, 16 / sizeof(T)>(p, v);
+    } else if (left >= 8 && width > 1) {
+        load8_as<T, 8 / sizeof(T)>(p, v);
+    } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) v[t] = t < left ? to_f32(p[t]) : 0.0f;
+    }
+}
+
+template <class T, int W>
+__device__ __forceinline__ void store8_as(T* p, const float v[8]) {
+#pragma unroll
+    for (int q = 0; q < 8 / W; ++q) {
+        Vec<T, W> x;
+#pragma unroll
+        for (int t = 0; t < W; ++t) x.v[t] = from_f32<T>(v[q * W + t]);
+        reinterpret_cast<Vec<T, W>*>(p)[q] = x;
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void store8(T* p, int left, int width, const float v[8]) {
+    if (left >= 8 && width == 16 / (int)sizeof(T)) {
+        store8_as<T, 16 / sizeof(T)>(p, v);
+    } else if (left >= 8 && width > 1) {
+        store8_as<T, 8 / sizeof(T)>(p, v);
+    } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            if (t < left) p[t] = from_f32<T>(v[t]);
+    }
+}
+
+// Division of 32-bit numbers by a fixed one, exact for every dividend below 2^31
+// (Granlund and Montgomery, "Division by invariant integers using multiplication",
+// PLDI 1994: with l = ceil(log2 div), m = floor(2^(31 + l) / div) + 1 has a relative
+// error of at most 2^-31 in the quotient's direction).
+struct FastDiv {
+    uint32_t div = 1;
+    uint64_t mul = 1ull << 31;
+    int shift = 31;
+    explicit FastDiv(uint32_t d) : div(d) {
+        int l = 0;
+        while ((1ull << l) < d) ++l;
+        shift = 31 + l;
+        mul = (1ull << shift) / d + 1;
+    }
+    __host__ __device__ __forceinline__ uint32_t quotient(uint32_t x) const { return (uint32_t)((x * mul) >> shift); }
+};
 
 // Where row i of a call goes (write) or comes from (read): row first + i, or slots[i].
 // Returns -1 for a row to leave out: slot -1 (padding), or a slot outside the matrix,
@@ -126,69 +193,91 @@ __global__ void k_block8_claim(const int64_t* __restrict__ slots, int64_t n, int
     }
 }
 
-// Whether row i is the one that stays in its slot s. Takes the whole warp.
+// Whether row i is the one that stays in its slot s. `lanes` (16 or 32) neighbouring
+// lanes ask for the same row, `lane` is this one's place among them; all lanes of the
+// warp call it together.
 __device__ __forceinline__ bool last_of_slot(const int64_t* __restrict__ slots, const int* __restrict__ claims,
-                                             int64_t i, int64_t n, int64_t s, int lane) {
-    if (!slots || s < 0) return true;
-    if (claims) return claims[s] == (int)i;
+                                             int64_t i, int64_t n, int64_t s, int lane, int lanes) {
+    if (claims) return s < 0 || claims[s] == (int)i;
     bool later = false;
-    for (int64_t j = i + 1 + lane; j < n; j += 32) later |= slots[j] == s;
-    return !__any_sync(0xFFFFFFFFu, later);
+    if (s >= 0)
+        for (int64_t j = i + 1 + lane; j < n; j += lanes) later |= slots[j] == s;
+    const uint32_t all = __ballot_sync(0xFFFFFFFFu, later);
+    const int shift = threadIdx.x & 31 & ~(lanes - 1);
+    return ((all >> shift) & (lanes == 32 ? 0xFFFFFFFFu : 0xFFFFu)) == 0u;
 }
 
-// Writes rows (values of a row contiguous, rows `ldx` apart). One warp takes four
-// consecutive (row, block) pairs at a time, 4 values of each block per lane: four
-// independent loads in flight per lane at every width (a row of 96 values alone is
-// one block), one redux.sync for a block's maximum, 128 bytes of codes per store.
+// The work of the row kernels: (row, block) pairs in row order, 16 lanes per pair with
+// 8 consecutive values each, two pairs per warp and step, kSteps steps in flight.
+// Short rows fill a warp as well as long ones (a row of 96 values is one pair).
+constexpr int kSteps = 4;
+constexpr int kPairsPerWarp = 2 * kSteps;
+
+// Writes rows (values of a row contiguous, rows `ldx` apart): a block's values are
+// read once, stay in registers, and leave as codes.
 template <class T>
 __global__ void __launch_bounds__(256)
-    k_block8_write(const T* __restrict__ X, int64_t n, int64_t d, int64_t ldx, int vec_ok,
-                   const int64_t* __restrict__ slots, int64_t first, const int* __restrict__ claims,
-                   uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t rows, int64_t pitch, int* status) {
+    k_block8_write(const T* __restrict__ X, int n, int d, int64_t ldx, int width, const int64_t* __restrict__ slots,
+                   int64_t first, const int* __restrict__ claims, uint8_t* __restrict__ codes,
+                   uint8_t* __restrict__ scales, int64_t rows, int pitch, FastDiv nb, int* status) {
     pdl_wait();
     pdl_release();
-    const int lane = threadIdx.x & 31;
-    const int64_t warp = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
-    const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    const int64_t nb = (d + kBlock - 1) / kBlock, groups = (nb + 3) / 4, total = n * nb;
-    for (int64_t f0 = warp * 4; f0 < total; f0 += nwarps * 4) {
-        int64_t row = total <= 0xFFFFFFFFll ? (int64_t)((uint32_t)f0 / (uint32_t)nb) : f0 / nb;
-        int64_t b = f0 - row * nb;
-        float v[4][4];
-        int64_t rr[4], bb[4];
+    const int lane = threadIdx.x & 31, half = lane >> 4, col8 = (lane & 15) * 8;
+    const uint32_t total = (uint32_t)n * nb.div;
+    const uint32_t stride = gridDim.x * (blockDim.x >> 5) * kPairsPerWarp;
+    const int groups = (int)(nb.div + 3) / 4;
+    for (uint32_t f0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kPairsPerWarp; f0 < total; f0 += stride) {
+        float v[kSteps][8];
+        uint32_t row[kSteps];
+        int64_t dest[kSteps];
+        int b[kSteps];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            rr[s] = f0 + s < total ? row : -1;
-            bb[s] = b;
-            if (++b == nb) {
-                b = 0;
-                ++row;
-            }
-            const int64_t col = bb[s] * kBlock + 4 * lane;
-            const T* src = X + rr[s] * ldx + col;
-            if (rr[s] >= 0 && vec_ok && col + 4 <= d) {
-                const Vec4<T> x = *reinterpret_cast<const Vec4<T>*>(src);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) v[s][t] = to_f32(x.v[t]);
-            } else {
-#pragma unroll
-                for (int t = 0; t < 4; ++t) v[s][t] = rr[s] >= 0 && col + t < d ? to_f32(src[t]) : 0.0f;
-            }
+        for (int s = 0; s < kSteps; ++s) {
+            const uint32_t f = f0 + 2 * s + half;
+            row[s] = nb.quotient(f);
+            b[s] = (int)(f - row[s] * nb.div);
+            dest[s] = f < total ? slot_of(slots, first, row[s], rows, status) : -1;
         }
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            if (rr[s] < 0) break;
-            const int64_t to = slot_of(slots, first, rr[s], rows, status);
-            if (to < 0 || !last_of_slot(slots, claims, rr[s], n, to, lane)) continue;
-            uint32_t a = 0u;
+        for (int s = 0; s < kSteps; ++s) {
+            const uint32_t f = f0 + 2 * s + half;
+            const int col = b[s] * kBlock + col8;
+            load8(X + (int64_t)row[s] * ldx + col, f < total ? d - col : 0, width, v[s]);
+        }
+        int mine = 0;       // lane 16 half + s keeps the exponent byte of step s
+        int64_t place = -1;
 #pragma unroll
-            for (int t = 0; t < 4; ++t) a = max(a, finite_magnitude(v[s][t]));
-            const int e = block_exponent(__reduce_max_sync(0xFFFFFFFFu, a));
+        for (int s = 0; s < kSteps; ++s) {
+            int64_t to = dest[s];
+            if (slots && !last_of_slot(slots, claims, row[s], n, to, lane & 15, 16)) to = -1;
+            float a = fabsf(v[s][0]);
+#pragma unroll
+            for (int t = 1; t < 8; ++t) a = fmaxf(a, fabsf(v[s][t]));  // (fmaxf passes over NaN)
+            uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, half ? 0u : __float_as_uint(a));
+            uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, half ? __float_as_uint(a) : 0u);
+            if (max(lo, hi) >= 0x7F800000u) {  // an infinity (or NaN alone): hold it as NaN, scale by the others
+                a = 0.0f;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    v[s][t] = finite_or_nan(v[s][t]);
+                    a = fmaxf(a, fabsf(v[s][t]));
+                }
+                lo = __reduce_max_sync(0xFFFFFFFFu, half ? 0u : __float_as_uint(a));
+                hi = __reduce_max_sync(0xFFFFFFFFu, half ? __float_as_uint(a) : 0u);
+            }
+            const int e = block_exponent(half ? hi : lo);
             const float inverse = __uint_as_float((uint32_t)(127 - e) << 23);
-            const int64_t col = bb[s] * kBlock + 4 * lane;
-            if (col < pitch) *reinterpret_cast<uint32_t*>(codes + to * pitch + col) = encode4(v[s], inverse);
-            if (lane == 0) scales[scale_at(to, bb[s], groups)] = (uint8_t)(e + 127);
+            const int col = b[s] * kBlock + col8;
+            if (to >= 0 && col < pitch) {
+                const uint2 c = make_uint2(encode4(v[s], inverse), encode4(v[s] + 4, inverse));
+                *reinterpret_cast<uint2*>(codes + to * pitch + col) = c;
+            }
+            if ((lane & 15) == s) {
+                mine = e + 127;
+                place = to < 0 ? -1 : scale_at(to, b[s], groups);
+            }
         }
+        if (place >= 0) scales[place] = (uint8_t)mine;
     }
 }
 
@@ -200,141 +289,144 @@ __global__ void __launch_bounds__(256)
 constexpr int kColRows = 64;
 
 template <class T>
-struct alignas(2 * sizeof(T)) Vec2 { T v[2]; };
-
-template <class T>
 __global__ void __launch_bounds__(256)
-    k_block8_write_cols(const T* __restrict__ X, int64_t n, int64_t d, int64_t ldx, int vec_ok,
+    k_block8_write_cols(const T* __restrict__ X, int n, int d, int64_t ldx, int vec_ok,
                         const int64_t* __restrict__ slots, int64_t first, const int* __restrict__ claims,
-                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t rows, int64_t pitch,
-                        int* status) {
-    constexpr int kPitch = kBlock + 4;
-    __shared__ uint32_t amax[8][kColRows];
+                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t rows, int pitch,
+                        FastDiv row_tiles, int* status) {
+    constexpr int kPitch = kBlock + 16;
+    __shared__ float amax[8][kColRows];
     __shared__ __align__(16) uint8_t turned[kColRows * kPitch];
+    __shared__ int64_t dest[kColRows];
     pdl_wait();
     pdl_release();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int64_t nb = (d + kBlock - 1) / kBlock, groups = (nb + 3) / 4;
-    const int64_t row_tiles = (n + kColRows - 1) / kColRows;
-    for (int64_t t = blockIdx.x; t < row_tiles * nb; t += gridDim.x) {
-        const int64_t b = t / row_tiles, i0 = (t - b * row_tiles) * kColRows + 2 * lane;
+    const int nb = (d + kBlock - 1) / kBlock, groups = (nb + 3) / 4;
+    const uint32_t tiles = row_tiles.div * (uint32_t)nb;
+    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int b = (int)row_tiles.quotient(t), base = (int)(t - (uint32_t)b * row_tiles.div) * kColRows;
+        const int i0 = base + 2 * lane, j0 = b * kBlock + 16 * w;
         float v[2][16];
-        uint32_t a[2] = {0u, 0u};
+        const T* src = X + (int64_t)j0 * ldx + i0;
+        if (vec_ok && i0 + 2 <= n && j0 + 16 <= d) {  // (no branch between the loads: all 16 are in flight together)
+            Vec<T, 2> x[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const int64_t j = b * kBlock + 16 * w + k;
-            const T* src = X + j * ldx + i0;
-            v[0][k] = v[1][k] = 0.0f;
-            if (j < d) {
-                if (vec_ok && i0 + 2 <= n) {
-                    const Vec2<T> x = *reinterpret_cast<const Vec2<T>*>(src);
-                    v[0][k] = to_f32(x.v[0]);
-                    v[1][k] = to_f32(x.v[1]);
-                } else {
-                    if (i0 < n) v[0][k] = to_f32(src[0]);
-                    if (i0 + 1 < n) v[1][k] = to_f32(src[1]);
+            for (int k = 0; k < 16; ++k) x[k] = *reinterpret_cast<const Vec<T, 2>*>(src + k * ldx);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                v[0][k] = to_f32(x[k].v[0]);
+                v[1][k] = to_f32(x[k].v[1]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                v[0][k] = j0 + k < d && i0 < n ? to_f32(src[k * ldx]) : 0.0f;
+                v[1][k] = j0 + k < d && i0 + 1 < n ? to_f32(src[k * ldx + 1]) : 0.0f;
+            }
+        }
+        // where the tile's rows go (8 rows per warp)
+        for (int r = w * (kColRows / 8); r < (w + 1) * (kColRows / 8); ++r) {
+            const int i = base + r;
+            int64_t to = i < n ? slot_of(slots, first, i, rows, status) : -1;
+            if (slots && !last_of_slot(slots, claims, i, n, to, lane, 32)) to = -1;
+            if (lane == 0) dest[r] = to;
+        }
+        float a[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) a[r] = fmaxf(a[r], fabsf(v[r][k]));
+            if (__float_as_uint(a[r]) >= 0x7F800000u) {  // (as in k_block8_write)
+                a[r] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    v[r][k] = finite_or_nan(v[r][k]);
+                    a[r] = fmaxf(a[r], fabsf(v[r][k]));
                 }
             }
         }
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            a[0] = max(a[0], finite_magnitude(v[0][k]));
-            a[1] = max(a[1], finite_magnitude(v[1][k]));
-        }
-        amax[w][2 * lane] = a[0];
-        amax[w][2 * lane + 1] = a[1];
+        *reinterpret_cast<float2*>(&amax[w][2 * lane]) = make_float2(a[0], a[1]);
         __syncthreads();
+        float m[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float2 x = *reinterpret_cast<const float2*>(&amax[q][2 * lane]);
+            m[0] = fmaxf(m[0], x.x);
+            m[1] = fmaxf(m[1], x.y);
+        }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            uint32_t m = 0u;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) m = max(m, amax[q][2 * lane + r]);
-            const int e = block_exponent(m);
+            const int e = block_exponent(__float_as_uint(m[r]));
             const float inverse = __uint_as_float((uint32_t)(127 - e) << 23);
-            uint32_t* dst = reinterpret_cast<uint32_t*>(turned + (2 * lane + r) * kPitch + 16 * w);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) dst[q] = encode4(&v[r][4 * q], inverse);
+            *reinterpret_cast<uint4*>(turned + (2 * lane + r) * kPitch + 16 * w) =
+                make_uint4(encode4(v[r], inverse), encode4(v[r] + 4, inverse), encode4(v[r] + 8, inverse),
+                           encode4(v[r] + 12, inverse));
+            if (w == r) {
+                const int64_t to = dest[2 * lane + r];
+                if (to >= 0) scales[scale_at(to, b, groups)] = (uint8_t)(e + 127);
+            }
         }
         __syncthreads();
-        // 8 rows per warp, 4 codes per lane
-        for (int r = 0; r < kColRows / 8; ++r) {
-            const int rl = w * (kColRows / 8) + r;
-            const int64_t i = (t - b * row_tiles) * kColRows + rl;
-            if (i >= n) break;
-            const int64_t to = slot_of(slots, first, i, rows, status);
-            if (to < 0 || !last_of_slot(slots, claims, i, n, to, lane)) continue;
-            const int64_t col = b * kBlock + 4 * lane;
-            if (col < pitch)
-                *reinterpret_cast<uint32_t*>(codes + to * pitch + col) =
-                    *reinterpret_cast<const uint32_t*>(turned + rl * kPitch + 4 * lane);
-            if (lane == 0) {
-                uint32_t m = 0u;
+        // 8 threads per row, 16 codes each
 #pragma unroll
-                for (int q = 0; q < 8; ++q) m = max(m, amax[q][rl]);
-                scales[scale_at(to, b, groups)] = (uint8_t)(block_exponent(m) + 127);
-            }
+        for (int q = 0; q < 2; ++q) {
+            const int r = (threadIdx.x >> 3) + 32 * q, c = (threadIdx.x & 7) * 16;
+            const int64_t to = dest[r];
+            if (to >= 0 && b * kBlock + c < pitch)
+                *reinterpret_cast<uint4*>(codes + to * pitch + b * kBlock + c) =
+                    *reinterpret_cast<const uint4*>(turned + r * kPitch + c);
         }
         __syncthreads();
     }
 }
 
-// Reads rows back, four (row, block) pairs per warp at a time as k_block8_write takes
-// them. Exact in fp32 and bf16; fp16 rounds to nearest even (and overflows to
-// infinity). Padding rows (slot -1) and rows outside the matrix read as zeros.
-// `ldo` columns are written for each row from d on up to `width` (zeros past d).
+// Reads rows back, pairs as in k_block8_write. Exact in fp32 and bf16; fp16 rounds to
+// nearest even (and overflows to infinity). Padding rows (slot -1) and rows outside
+// the matrix read as zeros. `columns` values are written for each row, zeros past d.
 template <class T>
 __global__ void __launch_bounds__(256)
-    k_block8_read(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int64_t pitch,
-                  int64_t d, const int64_t* __restrict__ slots, int64_t first, int64_t n, T* __restrict__ out,
-                  int64_t ldo, int64_t width, int vec_ok, int* status) {
+    k_block8_read(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int pitch,
+                  int d, const int64_t* __restrict__ slots, int64_t first, int n, T* __restrict__ out, int64_t ldo,
+                  int columns, int width, FastDiv nb, int* status) {
     pdl_wait();
     pdl_release();
-    const int lane = threadIdx.x & 31;
-    const int64_t warp = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
-    const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    const int64_t nb = (d + kBlock - 1) / kBlock, groups = (nb + 3) / 4, total = n * nb;
-    for (int64_t f0 = warp * 4; f0 < total; f0 += nwarps * 4) {
-        int64_t row = total <= 0xFFFFFFFFll ? (int64_t)((uint32_t)f0 / (uint32_t)nb) : f0 / nb;
-        int64_t b = f0 - row * nb;
-        uint32_t c[4];
-        float sc[4];
-        int64_t rr[4], bb[4];
+    const int lane = threadIdx.x & 31, half = lane >> 4, col8 = (lane & 15) * 8;
+    const uint32_t total = (uint32_t)n * nb.div;
+    const uint32_t stride = gridDim.x * (blockDim.x >> 5) * kPairsPerWarp;
+    const int groups = (int)(nb.div + 3) / 4;
+    for (uint32_t f0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kPairsPerWarp; f0 < total; f0 += stride) {
+        uint2 c[kSteps];
+        uint8_t byte[kSteps];
+        uint32_t row[kSteps];
+        int64_t from[kSteps];
+        int col[kSteps];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            rr[s] = f0 + s < total ? row : -1;
-            bb[s] = b;
-            if (++b == nb) {
-                b = 0;
-                ++row;
-            }
-            c[s] = 0u;
-            sc[s] = 0.0f;
-            if (rr[s] >= 0) {
-                const int64_t from = slot_of(slots, first, rr[s], rows, status);
-                const int64_t col = bb[s] * kBlock + 4 * lane;
-                if (from >= 0) {
-                    if (col < pitch) c[s] = *reinterpret_cast<const uint32_t*>(codes + from * pitch + col);
-                    sc[s] = scale_of(scales[scale_at(from, bb[s], groups)]);
-                }
-            }
+        for (int s = 0; s < kSteps; ++s) {
+            const uint32_t f = f0 + 2 * s + half;
+            row[s] = nb.quotient(f);
+            col[s] = (int)(f - row[s] * nb.div) * kBlock + col8;
+            from[s] = f < total ? slot_of(slots, first, row[s], rows, status) : -1;
+        }
+        // (a row that is left out loads row 0 and drops it, so that no branch parts the loads)
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int64_t r = max(from[s], (int64_t)0);
+            c[s] = *reinterpret_cast<const uint2*>(codes + r * pitch + min(col[s], pitch - 8));
+            byte[s] = scales[scale_at(r, col[s] / kBlock, groups)];
         }
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            if (rr[s] < 0) break;
-            float v[4];
-            decode4(c[s], v);
-            const int64_t col = bb[s] * kBlock + 4 * lane;
-            T* dst = out + rr[s] * ldo + col;
-            Vec4<T> o;
+        for (int s = 0; s < kSteps; ++s) {
+            float v[8];
+            decode4(c[s].x, v);
+            decode4(c[s].y, v + 4);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) o.v[t] = from_f32<T>(col + t < d ? v[t] * sc[s] : 0.0f);
-            if (vec_ok && col + 4 <= width) {
-                *reinterpret_cast<Vec4<T>*>(dst) = o;
-            } else {
+            for (int t = 0; t < 8; ++t) v[t] = from[s] >= 0 ? v[t] * scale_of(byte[s]) : 0.0f;
+            if (col[s] + 8 > d) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    if (col + t < width) dst[t] = o.v[t];
+                for (int t = 0; t < 8; ++t) v[t] = col[s] + t < d ? v[t] : 0.0f;
             }
+            const int left = f0 + 2 * s + half < total ? columns - col[s] : 0;
+            store8(out + (int64_t)row[s] * ldo + col[s], left, width, v);
         }
     }
 }
