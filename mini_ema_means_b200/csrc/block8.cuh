@@ -99,10 +99,9 @@ struct DeviceFacts {
 std::mutex g_b8_mu;
 DeviceFacts g_b8_dev[64];
 
-template <int BN, int OB, bool SWAP>
-bool b8_smem_attribute() {
-    return cudaFuncSetAttribute(b8::k_block8_matmul<BN, OB, SWAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                b8::MmCfg<BN>::kSmemBytes) == cudaSuccess;
+template <class K>
+bool b8_smem_attribute(K* kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
 }
 
 // The current device's SM count and clock; on the first call, its kernels' shared
@@ -118,8 +117,12 @@ int b8_device(int dev, DeviceFacts* out) {
         if (major != 10 || minor != 0) return fail(EM_E_NODEVICE, "this library is built for sm_100a (B200)");
         CK(cudaDeviceGetAttribute(&f.sms, cudaDevAttrMultiProcessorCount, dev));
         CK(cudaDeviceGetAttribute(&f.clock_khz, cudaDevAttrClockRate, dev));
-        if (!b8_smem_attribute<128, 4, false>() || !b8_smem_attribute<128, 2, false>() ||
-            !b8_smem_attribute<128, 4, true>() || !b8_smem_attribute<128, 2, true>()) {
+        if (!b8_smem_attribute(b8::k_block8_matmul<4, false>, b8::kSmem1) ||
+            !b8_smem_attribute(b8::k_block8_matmul<2, false>, b8::kSmem1) ||
+            !b8_smem_attribute(b8::k_block8_matmul<4, true>, b8::kSmem1) ||
+            !b8_smem_attribute(b8::k_block8_matmul<2, true>, b8::kSmem1) ||
+            !b8_smem_attribute(b8::k_block8_matmul_pair<4>, b8::kSmem2) ||
+            !b8_smem_attribute(b8::k_block8_matmul_pair<2>, b8::kSmem2)) {
             cudaGetLastError();
             return fail(EM_E_CUDA, "cudaFuncSetAttribute failed");
         }
@@ -193,20 +196,50 @@ static int read_block8(em_model* m, const em_block8_t* x, int64_t n, __nv_bfloat
 
 namespace {
 
-template <int BN, int OB, bool SWAP>
-int b8_launch_matmul(const em_block8_t* a, const em_block8_t* b, b8::MmArgs p, int sms, cudaStream_t st) {
-    CUtensorMap tmA, tmB;
+// Tensor map over a matrix's exponents: one row of 512 bytes for each 128 rows x 4 blocks.
+int b8_scale_map(CUtensorMap* tm, const em_block8_t* m) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(EM_E_CUDA, "cuTensorMapEncodeTiled is not available");
+    cuuint64_t dims[2] = {128, (cuuint64_t)((m->rows + 127) / 128 * b8_groups(m->d))};
+    cuuint64_t strides[1] = {b8::kAtomBytes};
+    cuuint32_t box[2] = {128, 1}, estr[2] = {1, 1};
+    CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, m->scales, dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(EM_E_CUDA, "cuTensorMapEncodeTiled (exponents) failed (%d)", (int)r);
+    return EM_OK;
+}
+
+// A product with the rows of `a` on the tiles' M side; `swap`: they are the output's columns.
+int b8_launch_matmul(const em_block8_t* a, int64_t na, const em_block8_t* b, int64_t nb, bool swap, b8::MmArgs p,
+                     size_t esz, int sms, cudaStream_t st) {
+    CUtensorMap tmA, tmB, tmSA, tmSB;
     CKR(make_tmap8(&tmA, a->codes, a->rows, (int)a->d, (int)b8_pitch(a->d), 128));
-    CKR(make_tmap8(&tmB, b->codes, b->rows, (int)b->d, (int)b8_pitch(b->d), BN));
-    p.sfa = static_cast<const uint8_t*>(a->scales);
-    p.sfb = static_cast<const uint8_t*>(b->scales);
-    p.n_atoms = (b->rows + 127) / 128;
+    CKR(make_tmap8(&tmB, b->codes, b->rows, (int)b->d, (int)b8_pitch(b->d), 128));
+    CKR(b8_scale_map(&tmSA, a));
+    CKR(b8_scale_map(&tmSB, b));
+    p.m_rows = na;
+    p.n_rows = nb;
     p.nkb = (int)b8_blocks(a->d);
-    p.m_tiles = (int)((p.m_rows + 127) / 128);
-    p.n_tiles = (int)((p.n_rows + BN - 1) / BN);
-    const int grid = (int)std::min<int64_t>((int64_t)p.m_tiles * p.n_tiles, sms);
-    CK(launch_k(true, b8::k_block8_matmul<BN, OB, SWAP>, dim3(grid), dim3(b8::kMmThreads), b8::MmCfg<BN>::kSmemBytes, st,
-                tmA, tmB, p));
+    // Pairs of CTAs with 256 x 256 tiles, or single ones with 128 x 128: the one whose
+    // longest CTA is shorter (per block 512 cycles a pair tile, about 400 a single one,
+    // which L2 feeds).
+    const int64_t t2 = ((na + 255) / 256) * ((nb + 255) / 256), t1 = ((na + 127) / 128) * ((nb + 127) / 128);
+    const int64_t pairs = std::max(sms / 2, 1);
+    if (!swap && (t2 + pairs - 1) / pairs * 512 <= (t1 + sms - 1) / sms * 400) {
+        p.m_tiles = (int)((na + 255) / 256);
+        p.n_tiles = (int)((nb + 255) / 256);
+        CK(launch_k(true, esz == 4 ? b8::k_block8_matmul_pair<4> : b8::k_block8_matmul_pair<2>,
+                    dim3((unsigned)(2 * std::min(t2, pairs))), dim3(b8::kPairThreads), b8::kSmem2, st, tmA, tmB, tmSA, tmSB,
+                    p));
+        return EM_OK;
+    }
+    p.m_tiles = (int)((na + 127) / 128);
+    p.n_tiles = (int)((nb + 127) / 128);
+    auto* kernel = esz == 4 ? (swap ? b8::k_block8_matmul<4, true> : b8::k_block8_matmul<4, false>)
+                            : (swap ? b8::k_block8_matmul<2, true> : b8::k_block8_matmul<2, false>);
+    CK(launch_k(true, kernel, dim3((unsigned)std::min<int64_t>(t1, sms)), dim3(b8::kMmThreads), b8::kSmem1, st, tmA, tmB,
+                tmSA, tmSB, p));
     return EM_OK;
 }
 
@@ -302,16 +335,9 @@ int em_block8_matmul(const em_block8_t* a, int64_t na, const em_block8_t* b, int
     p.status = a->status;
     const size_t esz = dtype_size(dtype);
     p.vec_ok = (uintptr_t)out % 16 == 0 && row_stride * esz % 16 == 0;
-    if (na <= 128 && nb > na) {  // few output rows: the rows of b take the tiles' 128 lanes
-        p.m_rows = nb;
-        p.n_rows = na;
-        return esz == 4 ? b8_launch_matmul<128, 4, true>(b, a, p, f.sms, st)
-                        : b8_launch_matmul<128, 2, true>(b, a, p, f.sms, st);
-    }
-    p.m_rows = na;
-    p.n_rows = nb;
-    return esz == 4 ? b8_launch_matmul<128, 4, false>(a, b, p, f.sms, st)
-                    : b8_launch_matmul<128, 2, false>(a, b, p, f.sms, st);
+    // few output rows: the rows of b take the tiles' 128 lanes
+    if (na <= 128 && nb > na) return b8_launch_matmul(b, nb, a, na, true, p, esz, f.sms, st);
+    return b8_launch_matmul(a, na, b, nb, false, p, esz, f.sms, st);
 }
 
 int em_block8_check(const em_block8_t* m, void* stream) {

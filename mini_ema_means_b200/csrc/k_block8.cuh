@@ -440,18 +440,26 @@ __global__ void __launch_bounds__(256)
 // block name the same byte (the scale-factor id of the instruction descriptor picks
 // byte block % 4 of the row's word), so one stored byte serves 128 values.
 //
-// One CTA per SM, persistent over output tiles of 128 x BN:
-//   warp 0     one thread loads 128 x 128 codes of A, BN x 128 of B (TMA, 128-byte
-//              swizzle) and the exponents of their rows into a ring of stages
+// The MMA's own accumulation cuts off below fp32's last place instead of rounding, an
+// error that grows with the number of steps (5.7e-7 of the result at d = 4096). So a
+// contraction is cut into spans of kSpan blocks: each starts a fresh accumulator, and
+// the epilogue adds the spans in order, rounding to nearest, in registers. Two
+// accumulators let it read one while the next span runs.
+//
+// Roles of a CTA's 10 warps:
+//   warp 0     one thread loads 128-byte-wide tiles of codes (TMA, 128-byte swizzle)
+//              and the exponents of their rows into a ring of stages
 //   warp 1     one thread copies a stage's exponents to tensor memory (each stage has
 //              its own columns there, so a copy never meets an MMA that still reads
-//              the last ones) and issues the MMAs into one of two accumulators
+//              the last ones) and issues the MMAs
 //   warps 2-9  epilogue: two groups of four warps (one per TMEM lane quadrant) take
 //              the left and right half of a tile's columns
-// SWAP: A is the operand whose rows are the output's columns (few output rows): a
-// lane then holds one output column and a warp stores 32 neighbours at once.
-// Otherwise a warp turns 32 rows x 128 bytes in shared memory and stores whole
-// 128-byte row pieces.
+
+constexpr int kMmThreads = 320;
+constexpr int kMmEpi = 256;
+constexpr int kSpan = 8;                      // blocks of 128 values per accumulator
+constexpr int kTurnBytes = 8 * 32 * 128;      // epilogue warps' turning buffers
+constexpr int kCodeTile = 128 * 128;          // codes of 128 rows x one block
 
 // Waits for a phase of `bar`; after `limit` clock cycles it raises EM_E_TIMEOUT and the
 // CTA's abort flag and gives up. (An error that an earlier call left in the matrix's
@@ -474,62 +482,51 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, long lon
     }
 }
 
-constexpr int kMmThreads = 320;
-constexpr int kMmEpi = 256;
-
-template <int BN>
-struct MmCfg {
-    static constexpr int kABytes = 128 * 128;
-    static constexpr int kBBytes = BN * 128;
-    static constexpr int kBAtoms = (BN + 127) / 128;
-    static constexpr int kSfBytes = (1 + kBAtoms) * kAtomBytes;
-    static constexpr int kStageBytes = kABytes + kBBytes + kSfBytes;
-    static constexpr int kTurnBytes = 8 * 32 * 128;  // epilogue warps' turning buffers
-    static constexpr int kFixed = 1024 + 256 + kTurnBytes;
-    static constexpr int kStages = (227 * 1024 - kFixed) / kStageBytes > 8 ? 8 : (227 * 1024 - kFixed) / kStageBytes;
-    static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
-    static constexpr int kSfCols = 4 * (1 + kBAtoms);  // tensor-memory columns of a stage's exponents
-    static constexpr int kSfBase = 2 * BN;
-    static_assert(kSfBase + kStages * kSfCols <= 512, "tensor memory");
-};
-
 // Instruction descriptor of tcgen05.mma kind::mxf8f6f4: the scale-factor ids in bits
 // 4-5 (B) and 29-30 (A), E4M3 operands (format 0 in bits 7-9 and 10-12), K-major (bits
 // 15, 16 = 0), N >> 3 in bits 17-22, E8M0 scales (bit 23), M >> 7 in bits 27-28.
-__device__ __forceinline__ uint32_t mm_idesc(int n, uint32_t sf_id) {
-    return (sf_id << 4) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | (1u << 27) | (sf_id << 29);
+__device__ __forceinline__ uint32_t mm_idesc(int m, int n, uint32_t sf_id) {
+    return (sf_id << 4) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 7) << 27) | (sf_id << 29);
 }
 
+template <int CG>
 __device__ __forceinline__ void umma_block8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                             uint32_t sfb, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+    if (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
 }
 
 // 512 bytes of exponents to four tensor-memory columns, repeated in each lane
-// quadrant. The descriptor: no swizzle, 8-row groups of 16-byte rows 128 bytes apart.
+// quadrant (CG = 2: in each CTA of the pair, from its own shared memory). The
+// descriptor: no swizzle, 8-row groups of 16-byte rows 128 bytes apart.
+template <int CG>
 __device__ __forceinline__ void copy_exponents(uint32_t tmem, uint32_t smem) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(tc::smem_desc(smem, 0ull, 128u))
-                 : "memory");
-}
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
+    if (CG == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem),
+                     "l"(tc::smem_desc(smem, 0ull, 128u))
+                     : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem),
+                     "l"(tc::smem_desc(smem, 0ull, 128u))
+                     : "memory");
 }
 
 struct MmArgs {
-    const uint8_t* sfa;   // exponents of the M operand, of the N operand
-    const uint8_t* sfb;
     void* out;
     int64_t ldo;
     int64_t m_rows, n_rows;  // rows of the M and N operands that the product takes
-    int64_t n_atoms;         // 128-row groups of the N operand's matrix
     int nkb;                 // blocks along the rows
     int m_tiles, n_tiles;
     int bf16;                // 16-bit results: bf16 rather than fp16
@@ -538,32 +535,132 @@ struct MmArgs {
     int* status;
 };
 
-// 32 fp32 accumulators of a lane as 32 / CPW output words (CPW = columns per word).
-__device__ __forceinline__ uint32_t pack_out(float lo, float hi, int bf16) {
+__device__ __forceinline__ uint32_t pack_out(uint32_t lo, uint32_t hi, int bf16) {
     uint32_t r;
     if (bf16) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+        const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
         memcpy(&r, &p, 4);
     } else {
-        const __half2 p = __floats2half2_rn(lo, hi);
+        const __half2 p = __floats2half2_rn(__uint_as_float(lo), __uint_as_float(hi));
         memcpy(&r, &p, 4);
     }
     return r;
 }
 
-template <int BN, int OB, bool SWAP>
+// Running sums of a lane's row start at -0, to which the first span adds exactly.
+// (Setting them from the first span instead made the compiler keep two copies.)
+template <int NS>
+__device__ __forceinline__ void clear_sums(uint32_t (&sum)[NS][32]) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) sum[i][e] = 0x80000000u;
+}
+
+// Adds 32 accumulator columns of this lane's row to its running sums.
+__device__ __forceinline__ void add_columns(uint32_t taddr, uint32_t (&sum)[32]) {
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+        uint32_t v[16];
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+            "%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+              "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+            : "r"(taddr + h)
+            : "memory");
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            sum[h + i] = __float_as_uint(__uint_as_float(sum[h + i]) + __uint_as_float(v[i]));
+    }
+}
+
+// One warp's 32 rows x 128 bytes of results (lane = row, 32 words w) to rows row0.. and
+// columns col0.. of `out`: turned in the warp's 4 KB of shared memory (16-byte pieces,
+// their place in the row XORed with the row, so that neither side meets a bank twice),
+// then stored as whole 128-byte row pieces, 8 lanes to a row.
+template <int OB>
+__device__ __forceinline__ void store_piece(const uint32_t (&w)[32], uint8_t* buf, int lane, int64_t row0, int64_t col0,
+                                            const MmArgs& p) {
+    if (col0 >= p.n_rows) return;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    __syncwarp();
+    const int64_t cc = col0 + (lane & 7) * (16 / OB);  // this lane's first column
+    uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + ((row0 + (lane >> 3)) * p.ldo + cc) * OB;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        const uint4 x = *reinterpret_cast<const uint4*>(buf + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+        if (row0 + r < p.m_rows) {
+            if (p.vec_ok && cc + 16 / OB <= p.n_rows) {
+                *reinterpret_cast<uint4*>(dst) = x;
+            } else {
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 16 / OB; ++e)
+                    if (cc + e < p.n_rows) {
+                        if (OB == 4)
+                            reinterpret_cast<uint32_t*>(dst)[e] = xs[e];
+                        else
+                            reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(xs[e >> 1] >> (16 * (e & 1)));
+                    }
+            }
+        }
+        dst += 4 * p.ldo * OB;
+    }
+}
+
+// A lane's NS x 32 results, column group i of them at col0 + 32 ((i + turn) % NS).
+template <int OB, int NS>
+__device__ __forceinline__ void store_rows(const uint32_t (&sum)[NS][32], int turn, uint8_t* buf, int lane, int64_t row0,
+                                           int64_t col0, const MmArgs& p) {
+    if (OB == 4) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) store_piece<OB>(sum[i], buf, lane, row0, col0 + 32 * ((i + turn) & (NS - 1)), p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS; i += 2) {
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                w[e] = pack_out(sum[i][2 * e], sum[i][2 * e + 1], p.bf16);
+                w[16 + e] = pack_out(sum[i + 1][2 * e], sum[i + 1][2 * e + 1], p.bf16);
+            }
+            store_piece<OB>(w, buf, lane, row0, col0 + 32 * ((i + turn) & (NS - 1)), p);
+        }
+    }
+}
+
+// ---- one CTA per 128 x 128 tile: few tiles, or few rows on one side
+//
+// SWAP: the M operand is the one whose rows are the output's columns (few output
+// rows): a lane holds one output column and a warp stores 32 neighbours at once.
+
+constexpr int kBN1 = 128;
+constexpr int kStage1 = 2 * kCodeTile + 2 * kAtomBytes;
+constexpr int kFixed1 = 1024 + 256 + kTurnBytes;
+constexpr int kStages1 = 5;
+constexpr int kSmem1 = kFixed1 + kStages1 * kStage1;
+constexpr int kSfCols1 = 8;
+static_assert(kSmem1 <= 227 * 1024 && 2 * kBN1 + kStages1 * kSfCols1 <= 512, "shared or tensor memory");
+
+template <int OB, bool SWAP>
 __global__ void __launch_bounds__(kMmThreads, 1)
-    k_block8_matmul(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const MmArgs p) {
-    using C = MmCfg<BN>;
+    k_block8_matmul(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, const MmArgs p) {
     using namespace tc;
-    constexpr int S = C::kStages;
+    constexpr int S = kStages1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
-    uint8_t* sB = sA + S * C::kABytes;
-    uint8_t* turn = sB + S * C::kBBytes;  // 128-byte aligned rows
-    uint8_t* sSf = turn + C::kTurnBytes;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sSf + S * C::kSfBytes);
+    uint8_t* sB = sA + S * kCodeTile;
+    uint8_t* turn = sB + S * kCodeTile;
+    uint8_t* sSf = turn + kTurnBytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sSf + S * 2 * kAtomBytes);
     uint64_t* full = bars;
     uint64_t* empty = bars + S;
     uint64_t* tfull = bars + 2 * S;
@@ -597,10 +694,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (warp == 0 && lane == 0) {
-        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmA) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmB) : "memory");
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -615,8 +708,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             bool ok = true;
             for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
                 const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
-                const int64_t atom_b = (int64_t)n * BN / 128;
-                const int atoms_b = (int)min((int64_t)C::kBAtoms, p.n_atoms - atom_b);
                 for (int kb = 0; kb < p.nkb; ++kb) {
                     if (!wait_bar(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag)) {
                         ok = false;
@@ -625,14 +716,12 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     const uint32_t fb = smem_u32(&full[stage]);
                     armed |= 1u << stage;
                     armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-                    mbar_expect_tx(fb, (uint32_t)(C::kABytes + C::kBBytes + (1 + atoms_b) * kAtomBytes));
-                    tma_load_2d(smem_u32(sA + stage * C::kABytes), &tmA, kb * kBlock, m * 128, fb);
-                    tma_load_2d(smem_u32(sB + stage * C::kBBytes), &tmB, kb * kBlock, n * BN, fb);
-                    uint8_t* sf = sSf + stage * C::kSfBytes;
-                    bulk_load(smem_u32(sf), p.sfa + ((int64_t)m * groups + (kb >> 2)) * kAtomBytes, kAtomBytes, fb);
-                    for (int q = 0; q < atoms_b; ++q)
-                        bulk_load(smem_u32(sf + (1 + q) * kAtomBytes),
-                                  p.sfb + ((atom_b + q) * groups + (kb >> 2)) * kAtomBytes, kAtomBytes, fb);
+                    mbar_expect_tx(fb, (uint32_t)kStage1);
+                    tma_load_2d(smem_u32(sA + stage * kCodeTile), &tmA, kb * kBlock, m * 128, fb);
+                    tma_load_2d(smem_u32(sB + stage * kCodeTile), &tmB, kb * kBlock, n * kBN1, fb);
+                    uint8_t* sf = sSf + stage * 2 * kAtomBytes;
+                    tma_load_2d(smem_u32(sf), &tmSA, 0, m * groups + (kb >> 2), fb);
+                    tma_load_2d(smem_u32(sf + kAtomBytes), &tmSB, 0, n * groups + (kb >> 2), fb);
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
@@ -649,38 +738,39 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
             for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                if (!wait_bar(smem_u32(&tempty[acc]), acc_phase ^ 1u, p.wait_limit, p.status, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
                 for (int kb = 0; kb < p.nkb; ++kb) {
+                    if (kb % kSpan == 0 &&
+                        !wait_bar(smem_u32(&tempty[acc]), acc_phase ^ 1u, p.wait_limit, p.status, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
                     if (!wait_bar(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sf = tmem_base + (uint32_t)(C::kSfBase + stage * C::kSfCols);
-                    const uint32_t ssf = smem_u32(sSf + stage * C::kSfBytes);
-#pragma unroll
-                    for (int q = 0; q < 1 + C::kBAtoms; ++q) copy_exponents(sf + 4 * q, ssf + q * kAtomBytes);
-                    const uint32_t a0 = smem_u32(sA + stage * C::kABytes), b0 = smem_u32(sB + stage * C::kBBytes);
-                    const uint32_t idesc = mm_idesc(BN, (uint32_t)(kb & 3));
+                    const uint32_t sf = tmem_base + (uint32_t)(2 * kBN1 + stage * kSfCols1);
+                    const uint32_t ssf = smem_u32(sSf + stage * 2 * kAtomBytes);
+                    copy_exponents<1>(sf, ssf);
+                    copy_exponents<1>(sf + 4, ssf + kAtomBytes);
+                    const uint32_t a0 = smem_u32(sA + stage * kCodeTile), b0 = smem_u32(sB + stage * kCodeTile);
+                    const uint32_t idesc = mm_idesc(128, kBN1, (uint32_t)(kb & 3));
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_block8(d_tmem, smem_desc(a0 + kk * 32, 2ull, 1024u), smem_desc(b0 + kk * 32, 2ull, 1024u),
-                                    idesc, sf, sf + 4, (kb | kk) != 0);
+                        umma_block8<1>(tmem_base + (uint32_t)(acc * kBN1), smem_desc(a0 + kk * 32, 2ull, 1024u),
+                                       smem_desc(b0 + kk * 32, 2ull, 1024u), idesc, sf, sf + 4,
+                                       (uint32_t)((kb % kSpan) | kk));
                     umma_commit(smem_u32(&empty[stage]));
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
                     }
+                    if (kb % kSpan == kSpan - 1 || kb == p.nkb - 1) {
+                        umma_commit(smem_u32(&tfull[acc]));
+                        acc ^= 1;
+                        if (acc == 0) acc_phase ^= 1u;
+                    }
                 }
-                if (!ok) break;
-                umma_commit(smem_u32(&tfull[acc]));
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1u;
             }
             if (!ok) {
                 umma_commit(smem_u32(drain));
@@ -694,89 +784,49 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         uint8_t* buf = turn + ew * 32 * 128;
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        bool ok = true;
+        for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
             const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
-            if (!__all_sync(0xFFFFFFFFu,
-                            wait_bar(smem_u32(&tfull[acc]), acc_phase, p.wait_limit, p.status, abort_flag)))
-                break;
-            tc_fence_after();
-            const uint32_t tbase = tmem_base + lane_base + (uint32_t)(acc * BN + half * (BN / 2));
             const int64_t row0 = (int64_t)m * 128 + 32 * q;
-            const int64_t col0 = (int64_t)n * BN + half * (BN / 2);
-            constexpr int kChunk = OB == 4 || SWAP ? 32 : 64;  // columns: 128 bytes of output row
-#pragma unroll
-            for (int c = 0; c < BN / 2; c += kChunk) {
-                uint32_t w[32];
-                if (kChunk == 32) {
-                    tmem_ld32(tbase + c, w);
-                    tmem_wait_ld32(w);
-                } else {
-                    uint32_t u[32];
-                    tmem_ld32(tbase + c, u);
-                    tmem_wait_ld32(u);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[i] = pack_out(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]), p.bf16);
-                    tmem_ld32(tbase + c + 32, u);
-                    tmem_wait_ld32(u);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[16 + i] = pack_out(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]), p.bf16);
+            const int64_t col0 = (int64_t)n * kBN1 + half * (kBN1 / 2);
+            uint32_t sum[2][32];
+            clear_sums(sum);
+            for (int kb = 0; kb < p.nkb; kb += kSpan) {
+                if (!__all_sync(0xFFFFFFFFu,
+                                wait_bar(smem_u32(&tfull[acc]), acc_phase, p.wait_limit, p.status, abort_flag))) {
+                    ok = false;
+                    break;
                 }
-                if (c + kChunk >= BN / 2) {  // the tile's last load is in registers
-                    tc_fence_before();
-                    mbar_arrive(smem_u32(&tempty[acc]));
-                }
-                if (SWAP) {
-                    const int64_t j = row0 + lane;  // output column
-                    if (j < p.m_rows) {
+                tc_fence_after();
+                const uint32_t tbase = tmem_base + lane_base + (uint32_t)(acc * kBN1 + half * (kBN1 / 2));
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int64_t r = col0 + c + i;  // output row
+                for (int i = 0; i < 2; ++i) add_columns(tbase + 32 * i, sum[i]);
+                tc_fence_before();
+                mbar_arrive(smem_u32(&tempty[acc]));
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            if (!ok) break;
+            if (SWAP) {
+                const int64_t j = row0 + lane;  // output column
+                if (j < p.m_rows) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int64_t r = col0 + 32 * i + e;  // output row
                             if (r < p.n_rows) {
                                 if (OB == 4)
-                                    reinterpret_cast<uint32_t*>(p.out)[r * p.ldo + j] = w[i];
+                                    reinterpret_cast<uint32_t*>(p.out)[r * p.ldo + j] = sum[i][e];
                                 else
                                     reinterpret_cast<uint16_t*>(p.out)[r * p.ldo + j] =
-                                        (uint16_t)pack_out(__uint_as_float(w[i]), 0.0f, p.bf16);
+                                        (uint16_t)pack_out(sum[i][e], 0u, p.bf16);
                             }
                         }
-                    }
-                } else {
-                    if (col0 + c >= p.n_rows) continue;
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) =
-                            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                    __syncwarp();
-                    const int64_t cc = col0 + c + (lane & 7) * (16 / OB);  // this lane's first column
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = 4 * i + (lane >> 3);
-                        const uint4 x = *reinterpret_cast<const uint4*>(buf + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-                        if (row0 + r < p.m_rows) {
-                            uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + ((row0 + r) * p.ldo + cc) * OB;
-                            if (p.vec_ok && cc + 16 / OB <= p.n_rows) {
-                                *reinterpret_cast<uint4*>(dst) = x;
-                            } else {
-                                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                                for (int e = 0; e < 16 / OB; ++e)
-                                    if (cc + e < p.n_rows) {
-                                        if (OB == 4)
-                                            reinterpret_cast<uint32_t*>(dst)[e] = xs[e];
-                                        else
-                                            reinterpret_cast<uint16_t*>(dst)[e] =
-                                                (uint16_t)(xs[e >> 1] >> (16 * (e & 1)));
-                                    }
-                            }
-                        }
-                    }
                 }
+            } else {
+                store_rows<OB, 2>(sum, 0, buf, lane, row0, col0, p);
             }
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1u;
         }
     }
 
@@ -786,6 +836,249 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         __syncwarp();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u) : "memory");
+    }
+}
+
+// ---- two CTAs per 256 x 256 tile (cta_group::2): large products
+//
+// Each CTA of a pair holds 128 rows of A and 128 of B, its half of the results (128
+// rows x 256 columns) and the exponents of its rows of A and of all 256 of B. Per
+// block of 128 values a CTA loads 33.5 KB for 512 cycles of MMA, a third less than a
+// lone CTA with a 128 x 256 tile, and L2 feeds that. The even CTA's one thread issues
+// the MMAs for both; loads of both CTAs complete on its barrier.
+//
+// Tensor memory: two accumulators of 256 columns would leave none for the exponents,
+// so the second starts at column kAcc2 and they share columns kAcc2 .. 255. Every
+// epilogue warp reads the 64 columns of its half that can be shared first (the right
+// half starts at its middle) and then lets the next span begin.
+
+// The epilogue's threads hold 128 running sums each, so the block is launched with a
+// third, mostly idle warpgroup whose registers they take over (setmaxnreg): 128 x 40 +
+// 256 x 216 = 60,416 of the 384 x 168 = 64,512 that the launch allots.
+constexpr int kPairThreads = 384;
+constexpr int kPairFewRegs = 40, kPairEpiRegs = 216;
+static_assert(128 * kPairFewRegs + 256 * kPairEpiRegs <= kPairThreads * 168, "registers");
+
+constexpr int kStages2 = 5;
+constexpr int kSf2 = 3 * kAtomBytes;
+constexpr int kStage2 = 2 * kCodeTile + kSf2;
+constexpr int kSmem2 = 1024 + 256 + kTurnBytes + kStages2 * kStage2;
+constexpr int kSfCols2 = 12;
+constexpr int kAcc2 = 192;
+constexpr int kSfBase2 = kAcc2 + 256;
+static_assert(kSmem2 <= 227 * 1024 && kSfBase2 + kStages2 * kSfCols2 <= 512, "shared or tensor memory");
+
+// The address of `addr` (this CTA's shared memory) in the pair's even CTA.
+__device__ __forceinline__ uint32_t in_even_cta(uint32_t addr) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+
+// A load into this CTA's shared memory that completes on a barrier of the pair's even CTA.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(dst),
+        "l"((uint64_t)tm), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// Arrival on the same barrier of both CTAs once the MMAs issued so far are done.
+__device__ __forceinline__ void commit_both(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+template <int OB>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    k_block8_matmul_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                         const MmArgs p) {
+    using namespace tc;
+    constexpr int S = kStages2;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = sA + S * kCodeTile;
+    uint8_t* turn = sB + S * kCodeTile;
+    uint8_t* sSf = turn + kTurnBytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sSf + S * kSf2);
+    uint64_t* full = bars;            // (even CTA) both CTAs' loads of a stage
+    uint64_t* empty = bars + S;       // (each CTA) the MMAs are done with a stage
+    uint64_t* tfull = bars + 2 * S;   // (each CTA) a span's accumulator is complete
+    uint64_t* shared = tfull + 1;     // (even CTA) both CTAs have read the shared columns
+    uint64_t* drain = tfull + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 3);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const long long drain_limit = p.wait_limit > 4000000000ll ? p.wait_limit : 4000000000ll;
+    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int groups = (p.nkb + 3) / 4;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        mbar_init(smem_u32(tfull), 1);
+        mbar_init(smem_u32(shared), 2 * kMmEpi / 32);
+        mbar_init(smem_u32(drain), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();
+    pdl_release();
+
+    // (each role's code lies inside the branch that sets its registers: code after a
+    // join would have to do with the fewer)
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairFewRegs));
+        if (warp == 0 && lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, armed = 0, armed_parity = 0;
+            bool ok = true;
+            for (int64_t t = first; t < tiles && ok; t += step) {
+                const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
+                const int am = 2 * m + (int)rank, bn = 2 * n + (int)rank;  // this CTA's 128-row groups
+                for (int kb = 0; kb < p.nkb; ++kb) {
+                    if (!wait_bar(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    armed |= 1u << stage;
+                    armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                    if (rank == 0) mbar_expect_tx(smem_u32(&full[stage]), (uint32_t)(2 * kStage2));
+                    const uint32_t fb = in_even_cta(smem_u32(&full[stage]));
+                    tma_load_pair(smem_u32(sA + stage * kCodeTile), &tmA, kb * kBlock, am * 128, fb);
+                    tma_load_pair(smem_u32(sB + stage * kCodeTile), &tmB, kb * kBlock, bn * 128, fb);
+                    uint8_t* sf = sSf + stage * kSf2;
+                    tma_load_pair(smem_u32(sf), &tmSA, 0, am * groups + (kb >> 2), fb);
+                    tma_load_pair(smem_u32(sf + kAtomBytes), &tmSB, 0, 2 * n * groups + (kb >> 2), fb);
+                    tma_load_pair(smem_u32(sf + 2 * kAtomBytes), &tmSB, 0, (2 * n + 1) * groups + (kb >> 2), fb);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // (the even CTA's barriers stand for both CTAs' loads; neither CTA leaves
+            // before the other, see the end)
+            if (!ok && rank == 0)
+                for (int s = 0; s < S; ++s)
+                    if (armed & (1u << s)) mbar_drain(smem_u32(&full[s]), (armed_parity >> s) & 1u, drain_limit);
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            int stage = 0;
+            uint32_t phase = 0, span = 0;  // spans issued
+            bool ok = true;
+            for (int64_t t = first; t < tiles && ok; t += step) {
+                for (int kb = 0; kb < p.nkb; ++kb) {
+                    if (kb % kSpan == 0 && span > 0 &&
+                        !wait_bar(smem_u32(shared), (span - 1) & 1u, p.wait_limit, p.status, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (!wait_bar(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sf = tmem_base + (uint32_t)(kSfBase2 + stage * kSfCols2);
+                    const uint32_t ssf = smem_u32(sSf + stage * kSf2);
+#pragma unroll
+                    for (int q = 0; q < 3; ++q) copy_exponents<2>(sf + 4 * q, ssf + q * kAtomBytes);
+                    const uint32_t a0 = smem_u32(sA + stage * kCodeTile), b0 = smem_u32(sB + stage * kCodeTile);
+                    const uint32_t idesc = mm_idesc(256, 256, (uint32_t)(kb & 3));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_block8<2>(tmem_base + (span & 1u) * kAcc2, smem_desc(a0 + kk * 32, 2ull, 1024u),
+                                       smem_desc(b0 + kk * 32, 2ull, 1024u), idesc, sf, sf + 4,
+                                       (uint32_t)((kb % kSpan) | kk));
+                    commit_both(smem_u32(&empty[stage]));
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (kb % kSpan == kSpan - 1 || kb == p.nkb - 1) {
+                        commit_both(smem_u32(tfull));
+                        ++span;
+                    }
+                }
+            }
+            if (!ok) {
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                 smem_u32(drain))
+                             : "memory");
+                mbar_drain(smem_u32(drain), 0u, drain_limit);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairEpiRegs));
+        const int ew = warp - 4;
+        const int q = warp & 3, half = ew >> 2;
+        const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+        uint8_t* buf = turn + ew * 32 * 128;
+        const uint32_t shared_bar = in_even_cta(smem_u32(shared));
+        uint32_t span = 0;
+        bool ok = true;
+        for (int64_t t = first; t < tiles && ok; t += step) {
+            const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
+            const int64_t row0 = (int64_t)m * 256 + rank * 128 + 32 * q;
+            const int64_t col0 = (int64_t)n * 256 + half * 128;
+            uint32_t sum[4][32];  // columns col0 + 32 ((i + 2 half) % 4)
+            clear_sums(sum);
+            for (int kb = 0; kb < p.nkb; kb += kSpan) {
+                if (!__all_sync(0xFFFFFFFFu,
+                                wait_bar(smem_u32(tfull), span & 1u, p.wait_limit, p.status, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t tbase = tmem_base + lane_base + (span & 1u) * kAcc2 + (uint32_t)(half * 128);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    add_columns(tbase + 32 * ((i + 2 * half) & 3), sum[i]);
+                    if (i == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(shared_bar)
+                                         : "memory");
+                    }
+                }
+                ++span;
+            }
+            if (!ok) break;
+            store_rows<OB, 4>(sum, 2 * half, buf, lane, row0, col0, p);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    // neither CTA's shared or tensor memory goes while the other may still use it
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u) : "memory");
     }
 }
 
