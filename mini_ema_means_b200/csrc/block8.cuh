@@ -210,28 +210,48 @@ int b8_scale_map(CUtensorMap* tm, const em_block8_t* m) {
     return EM_OK;
 }
 
+// Tensor map over the result for the pair kernel's stores: boxes of 32 rows x 128 bytes.
+int b8_out_map(CUtensorMap* tm, const b8::MmArgs& p, size_t esz) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(EM_E_CUDA, "cuTensorMapEncodeTiled is not available");
+    cuuint64_t dims[2] = {(cuuint64_t)p.n_rows, (cuuint64_t)p.m_rows};
+    cuuint64_t strides[1] = {(cuuint64_t)p.ldo * esz};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / esz), 32}, estr[2] = {1, 1};
+    CUresult r = fn(tm, esz == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, p.out, dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(EM_E_CUDA, "cuTensorMapEncodeTiled (result) failed (%d)", (int)r);
+    return EM_OK;
+}
+
 // A product with the rows of `a` on the tiles' M side; `swap`: they are the output's columns.
 int b8_launch_matmul(const em_block8_t* a, int64_t na, const em_block8_t* b, int64_t nb, bool swap, b8::MmArgs p,
                      size_t esz, int sms, cudaStream_t st) {
+    // Pairs of CTAs with 256 x 192 tiles, or single ones with 128 x 128: the one whose
+    // longest CTA is shorter (per block 384 cycles a pair tile, about 400 a single one,
+    // which L2 feeds).
+    const int64_t t1 = ((na + 127) / 128) * ((nb + 127) / 128);
+    const int64_t t2 = ((na + 255) / 256) * ((nb + b8::kPairN - 1) / b8::kPairN);
+    const int64_t pairs = std::max(sms / 2, 1);
+    const bool pair = !swap && (t2 + pairs - 1) / pairs * 384 <= (t1 + sms - 1) / sms * 400;
     CUtensorMap tmA, tmB, tmSA, tmSB;
     CKR(make_tmap8(&tmA, a->codes, a->rows, (int)a->d, (int)b8_pitch(a->d), 128));
-    CKR(make_tmap8(&tmB, b->codes, b->rows, (int)b->d, (int)b8_pitch(b->d), 128));
+    CKR(make_tmap8(&tmB, b->codes, b->rows, (int)b->d, (int)b8_pitch(b->d), pair ? b8::kPairN / 2 : 128));
     CKR(b8_scale_map(&tmSA, a));
     CKR(b8_scale_map(&tmSB, b));
     p.m_rows = na;
     p.n_rows = nb;
     p.nkb = (int)b8_blocks(a->d);
-    // Pairs of CTAs with 256 x 256 tiles, or single ones with 128 x 128: the one whose
-    // longest CTA is shorter (per block 512 cycles a pair tile, about 400 a single one,
-    // which L2 feeds).
-    const int64_t t2 = ((na + 255) / 256) * ((nb + 255) / 256), t1 = ((na + 127) / 128) * ((nb + 127) / 128);
-    const int64_t pairs = std::max(sms / 2, 1);
-    if (!swap && (t2 + pairs - 1) / pairs * 512 <= (t1 + sms - 1) / sms * 400) {
+    if (pair) {
         p.m_tiles = (int)((na + 255) / 256);
-        p.n_tiles = (int)((nb + 255) / 256);
+        p.n_tiles = (int)((nb + b8::kPairN - 1) / b8::kPairN);
+        // (strides of a tensor map end below 2^40 bytes)
+        if (p.ldo * (int64_t)esz >= (1ll << 40)) p.vec_ok = 0;
+        CUtensorMap tmOut = tmA;  // not used where the result's rows are not aligned
+        if (p.vec_ok) CKR(b8_out_map(&tmOut, p, esz));
         CK(launch_k(true, esz == 4 ? b8::k_block8_matmul_pair<4> : b8::k_block8_matmul_pair<2>,
                     dim3((unsigned)(2 * std::min(t2, pairs))), dim3(b8::kPairThreads), b8::kSmem2, st, tmA, tmB, tmSA, tmSB,
-                    p));
+                    tmOut, p));
         return EM_OK;
     }
     p.m_tiles = (int)((na + 127) / 128);

@@ -449,9 +449,10 @@ __global__ void __launch_bounds__(256)
 // Roles of a CTA's 10 warps:
 //   warp 0     one thread loads 128-byte-wide tiles of codes (TMA, 128-byte swizzle)
 //              and the exponents of their rows into a ring of stages
-//   warp 1     one thread copies a stage's exponents to tensor memory (each stage has
-//              its own columns there, so a copy never meets an MMA that still reads
-//              the last ones) and issues the MMAs
+//   warp 1     one thread issues the MMAs and, every fourth block, copies the exponents
+//              of four blocks to tensor memory. They go round as many sets of columns
+//              there as the ring has stages: a set's last user is at least that many
+//              blocks back, and the wait for this block's stage was a wait for it
 //   warps 2-9  epilogue: two groups of four warps (one per TMEM lane quadrant) take
 //              the left and right half of a tile's columns
 
@@ -461,16 +462,31 @@ constexpr int kSpan = 8;                      // blocks of 128 values per accumu
 constexpr int kTurnBytes = 8 * 32 * 128;      // epilogue warps' turning buffers
 constexpr int kCodeTile = 128 * 128;          // codes of 128 rows x one block
 
-// Waits for a phase of `bar`; after `limit` clock cycles it raises EM_E_TIMEOUT and the
-// CTA's abort flag and gives up. (An error that an earlier call left in the matrix's
-// status word, an out-of-range slot say, does not stop a product: only this CTA's own
-// waits do.)
+template <bool CLUSTER>
+__device__ __forceinline__ bool try_bar(uint32_t bar, uint32_t parity) {
+    if (!CLUSTER) return tc::mbar_try_wait(bar, parity);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Waits for a phase of `bar` (CLUSTER: the other CTA of the pair may arrive on it);
+// after `limit` clock cycles it raises EM_E_TIMEOUT and the CTA's abort flag and gives
+// up. (An error that an earlier call left in the matrix's status word, an out-of-range
+// slot say, does not stop a product: only this CTA's own waits do.)
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, long long limit, int* status,
                                          volatile int* abort_flag) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
+    if (try_bar<CLUSTER>(bar, parity)) return true;
     const long long t0 = clock64();
     for (uint32_t it = 1;; ++it) {
-        if (tc::mbar_try_wait(bar, parity)) return true;
+        if (try_bar<CLUSTER>(bar, parity)) return true;
         if ((it & 63u) == 0) {
             if (*abort_flag) return false;
             if (clock64() - t0 > limit) {
@@ -480,6 +496,19 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, long lon
             }
         }
     }
+}
+
+// One lane of a converged warp. The issuing warps walk their loops with all lanes and
+// let one issue: the loop's values stay warp-uniform, and the MMA's operands with them
+// (under a branch on the lane the issue itself took longer than the MMAs).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r));
+    return r != 0;
 }
 
 // Instruction descriptor of tcgen05.mma kind::mxf8f6f4: the scale-factor ids in bits
@@ -575,26 +604,28 @@ __device__ __forceinline__ void add_columns(uint32_t taddr, uint32_t (&sum)[32])
     }
 }
 
-// One warp's 32 rows x 128 bytes of results (lane = row, 32 words w) to rows row0.. and
-// columns col0.. of `out`: turned in the warp's 4 KB of shared memory (16-byte pieces,
-// their place in the row XORed with the row, so that neither side meets a bank twice),
-// then stored as whole 128-byte row pieces, 8 lanes to a row.
-template <int OB>
+// One warp's 32 rows x Q 16-byte pieces of results (lane = row, 4 Q words w) to rows
+// row0.. and columns col0.. of `out`: turned in the warp's 4 KB of shared memory (a
+// piece's place in its row XORed with the row, so that neither side meets a bank
+// twice), then stored as whole 128-byte row pieces (64 with Q = 4), Q lanes to a row.
+template <int OB, int Q>
 __device__ __forceinline__ void store_piece(const uint32_t (&w)[32], uint8_t* buf, int lane, int64_t row0, int64_t col0,
                                             const MmArgs& p) {
     if (col0 >= p.n_rows) return;
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < Q; ++i)
         *reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) =
             make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     __syncwarp();
-    const int64_t cc = col0 + (lane & 7) * (16 / OB);  // this lane's first column
-    uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + ((row0 + (lane >> 3)) * p.ldo + cc) * OB;
+    constexpr int kRows = 32 / Q;  // rows per step
+    const int piece = lane % Q, r0 = lane / Q;
+    const int64_t cc = col0 + piece * (16 / OB);  // this lane's first column
+    uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + ((row0 + r0) * p.ldo + cc) * OB;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 3);
-        const uint4 x = *reinterpret_cast<const uint4*>(buf + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+    for (int i = 0; i < Q; ++i) {
+        const int r = kRows * i + r0;
+        const uint4 x = *reinterpret_cast<const uint4*>(buf + r * 128 + ((piece ^ (r & 7)) << 4));
         if (row0 + r < p.m_rows) {
             if (p.vec_ok && cc + 16 / OB <= p.n_rows) {
                 *reinterpret_cast<uint4*>(dst) = x;
@@ -610,17 +641,17 @@ __device__ __forceinline__ void store_piece(const uint32_t (&w)[32], uint8_t* bu
                     }
             }
         }
-        dst += 4 * p.ldo * OB;
+        dst += kRows * p.ldo * OB;
     }
 }
 
-// A lane's NS x 32 results, column group i of them at col0 + 32 ((i + turn) % NS).
+// A lane's NS x 32 results from column col0 on.
 template <int OB, int NS>
-__device__ __forceinline__ void store_rows(const uint32_t (&sum)[NS][32], int turn, uint8_t* buf, int lane, int64_t row0,
+__device__ __forceinline__ void store_rows(const uint32_t (&sum)[NS][32], uint8_t* buf, int lane, int64_t row0,
                                            int64_t col0, const MmArgs& p) {
     if (OB == 4) {
 #pragma unroll
-        for (int i = 0; i < NS; ++i) store_piece<OB>(sum[i], buf, lane, row0, col0 + 32 * ((i + turn) & (NS - 1)), p);
+        for (int i = 0; i < NS; ++i) store_piece<OB, 8>(sum[i], buf, lane, row0, col0 + 32 * i, p);
     } else {
 #pragma unroll
         for (int i = 0; i < NS; i += 2) {
@@ -628,9 +659,12 @@ __device__ __forceinline__ void store_rows(const uint32_t (&sum)[NS][32], int tu
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 w[e] = pack_out(sum[i][2 * e], sum[i][2 * e + 1], p.bf16);
-                w[16 + e] = pack_out(sum[i + 1][2 * e], sum[i + 1][2 * e + 1], p.bf16);
+                if (i + 1 < NS) w[16 + e] = pack_out(sum[i + 1 < NS ? i + 1 : i][2 * e], sum[i + 1 < NS ? i + 1 : i][2 * e + 1], p.bf16);
             }
-            store_piece<OB>(w, buf, lane, row0, col0 + 32 * ((i + turn) & (NS - 1)), p);
+            if (i + 1 < NS)
+                store_piece<OB, 8>(w, buf, lane, row0, col0 + 32 * i, p);
+            else
+                store_piece<OB, 4>(w, buf, lane, row0, col0 + 32 * i, p);
         }
     }
 }
@@ -716,12 +750,14 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     const uint32_t fb = smem_u32(&full[stage]);
                     armed |= 1u << stage;
                     armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-                    mbar_expect_tx(fb, (uint32_t)kStage1);
+                    mbar_expect_tx(fb, (uint32_t)((kb & 3) == 0 ? kStage1 : 2 * kCodeTile));
                     tma_load_2d(smem_u32(sA + stage * kCodeTile), &tmA, kb * kBlock, m * 128, fb);
                     tma_load_2d(smem_u32(sB + stage * kCodeTile), &tmB, kb * kBlock, n * kBN1, fb);
-                    uint8_t* sf = sSf + stage * 2 * kAtomBytes;
-                    tma_load_2d(smem_u32(sf), &tmSA, 0, m * groups + (kb >> 2), fb);
-                    tma_load_2d(smem_u32(sf + kAtomBytes), &tmSB, 0, n * groups + (kb >> 2), fb);
+                    if ((kb & 3) == 0) {
+                        uint8_t* sf = sSf + stage * 2 * kAtomBytes;
+                        tma_load_2d(smem_u32(sf), &tmSA, 0, m * groups + (kb >> 2), fb);
+                        tma_load_2d(smem_u32(sf + kAtomBytes), &tmSB, 0, n * groups + (kb >> 2), fb);
+                    }
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
@@ -734,7 +770,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            int stage = 0, acc = 0;
+            int stage = 0, acc = 0, slot = S - 1;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
             for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
@@ -749,10 +785,13 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sf = tmem_base + (uint32_t)(2 * kBN1 + stage * kSfCols1);
-                    const uint32_t ssf = smem_u32(sSf + stage * 2 * kAtomBytes);
-                    copy_exponents<1>(sf, ssf);
-                    copy_exponents<1>(sf + 4, ssf + kAtomBytes);
+                    if ((kb & 3) == 0 && ++slot == S) slot = 0;
+                    const uint32_t sf = tmem_base + (uint32_t)(2 * kBN1 + slot * kSfCols1);
+                    if ((kb & 3) == 0) {
+                        const uint32_t ssf = smem_u32(sSf + stage * 2 * kAtomBytes);
+                        copy_exponents<1>(sf, ssf);
+                        copy_exponents<1>(sf + 4, ssf + kAtomBytes);
+                    }
                     const uint32_t a0 = smem_u32(sA + stage * kCodeTile), b0 = smem_u32(sB + stage * kCodeTile);
                     const uint32_t idesc = mm_idesc(128, kBN1, (uint32_t)(kb & 3));
 #pragma unroll
@@ -825,7 +864,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                         }
                 }
             } else {
-                store_rows<OB, 2>(sum, 0, buf, lane, row0, col0, p);
+                store_rows<OB, 2>(sum, buf, lane, row0, col0, p);
             }
         }
     }
@@ -839,34 +878,38 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     }
 }
 
-// ---- two CTAs per 256 x 256 tile (cta_group::2): large products
+// ---- two CTAs per 256 x 192 tile (cta_group::2): large products
 //
-// Each CTA of a pair holds 128 rows of A and 128 of B, its half of the results (128
-// rows x 256 columns) and the exponents of its rows of A and of all 256 of B. Per
-// block of 128 values a CTA loads 33.5 KB for 512 cycles of MMA, a third less than a
-// lone CTA with a 128 x 256 tile, and L2 feeds that. The even CTA's one thread issues
-// the MMAs for both; loads of both CTAs complete on its barrier.
+// Each CTA of a pair holds 128 rows of A and 96 of B, its half of the results (128
+// rows x 192 columns) and the exponents of its rows of A and of all 192 of B: 28 KB of
+// codes for 384 cycles of MMA, where a lone CTA would load 40. The even CTA's one
+// thread issues the MMAs for both; loads of both CTAs complete on its barrier.
 //
-// Tensor memory: two accumulators of 256 columns would leave none for the exponents,
-// so the second starts at column kAcc2 and they share columns kAcc2 .. 255. Every
-// epilogue warp reads the 64 columns of its half that can be shared first (the right
-// half starts at its middle) and then lets the next span begin.
+// 192 columns, because two accumulators of 256 leave no tensor memory for the
+// exponents: sharing 64 columns between them made each span wait for the epilogue's
+// first reads through two cluster-wide barriers, 0.8 us a span (8,192 x 8,192 x 4,096:
+// 253 us). A tile starts in the middle of a 128-row group of exponents every other
+// time; the MMA then takes them from two columns on.
+//
+// A stage of the ring holds two blocks: a barrier round trip for each block alone took
+// the issuing warp as long as its MMAs do. 12 epilogue warps (warps 2-13) take 64
+// columns each; a piece of 32 rows x 128 bytes leaves through a TMA store (store_piece
+// where the result's rows are not 16-byte aligned).
 
-// The epilogue's threads hold 128 running sums each, so the block is launched with a
-// third, mostly idle warpgroup whose registers they take over (setmaxnreg): 128 x 40 +
-// 256 x 216 = 60,416 of the 384 x 168 = 64,512 that the launch allots.
-constexpr int kPairThreads = 384;
-constexpr int kPairFewRegs = 40, kPairEpiRegs = 216;
-static_assert(128 * kPairFewRegs + 256 * kPairEpiRegs <= kPairThreads * 168, "registers");
-
-constexpr int kStages2 = 5;
+constexpr int kPairN = 192;
+constexpr int kPairEpiWarps = 12;
+constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
+constexpr int kPerStage = 2;
+constexpr int kStages2 = 3;
+constexpr int kTurnBytes2 = kPairEpiWarps * 32 * 128;
+constexpr int kCodeTileB2 = kPairN / 2 * 128;
 constexpr int kSf2 = 3 * kAtomBytes;
-constexpr int kStage2 = 2 * kCodeTile + kSf2;
-constexpr int kSmem2 = 1024 + 256 + kTurnBytes + kStages2 * kStage2;
+constexpr int kCodes2 = kCodeTile + kCodeTileB2;  // codes of one block
+constexpr int kSmem2 = 1024 + 256 + kTurnBytes2 + kStages2 * (kPerStage * kCodes2 + kSf2);
 constexpr int kSfCols2 = 12;
-constexpr int kAcc2 = 192;
-constexpr int kSfBase2 = kAcc2 + 256;
+constexpr int kSfBase2 = 2 * kPairN;
 static_assert(kSmem2 <= 227 * 1024 && kSfBase2 + kStages2 * kSfCols2 <= 512, "shared or tensor memory");
+static_assert(4 % kPerStage == 0 && kSpan % 4 == 0, "a stage lies within a group of exponents, a group within a span");
 
 // The address of `addr` (this CTA's shared memory) in the pair's even CTA.
 __device__ __forceinline__ uint32_t in_even_cta(uint32_t addr) {
@@ -884,6 +927,10 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* t
         : "memory");
 }
 
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // Arrival on the same barrier of both CTAs once the MMAs issued so far are done.
 __device__ __forceinline__ void commit_both(uint32_t bar) {
     asm volatile(
@@ -892,26 +939,49 @@ __device__ __forceinline__ void commit_both(uint32_t bar) {
         : "memory");
 }
 
+// store_piece through the TMA unit: the warp's turning buffer is its shared-memory box
+// (32 rows x 128 bytes, 128-byte swizzle, which is the XOR of store_piece); rows past
+// the result are left out by the tensor map. The store reads the buffer while the warp
+// goes on; the next one waits for that.
+__device__ __forceinline__ void store_tma(const uint32_t (&w)[32], uint8_t* buf, int lane, int row0, int col0,
+                                          const CUtensorMap* tm) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                         (uint64_t)tm),
+                     "r"(col0), "r"(row0), "r"(tc::smem_u32(buf))
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+}
+
 template <int OB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_block8_matmul_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
-                         const MmArgs p) {
+                         const __grid_constant__ CUtensorMap tmOut, const MmArgs p) {
     using namespace tc;
     constexpr int S = kStages2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
-    uint8_t* sB = sA + S * kCodeTile;
-    uint8_t* turn = sB + S * kCodeTile;
-    uint8_t* sSf = turn + kTurnBytes;
+    uint8_t* sB = sA + S * kPerStage * kCodeTile;
+    uint8_t* turn = sB + S * kPerStage * kCodeTileB2;
+    uint8_t* sSf = turn + kTurnBytes2;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sSf + S * kSf2);
     uint64_t* full = bars;            // (even CTA) both CTAs' loads of a stage
     uint64_t* empty = bars + S;       // (each CTA) the MMAs are done with a stage
-    uint64_t* tfull = bars + 2 * S;   // (each CTA) a span's accumulator is complete
-    uint64_t* shared = tfull + 1;     // (even CTA) both CTAs have read the shared columns
-    uint64_t* drain = tfull + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 3);
+    uint64_t* tfull = bars + 2 * S;   // (each CTA) an accumulator is complete
+    uint64_t* tempty = tfull + 2;     // (even CTA) both CTAs have read an accumulator
+    uint64_t* drain = tfull + 4;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 5);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -927,8 +997,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
-        mbar_init(smem_u32(tfull), 1);
-        mbar_init(smem_u32(shared), 2 * kMmEpi / 32);
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&tfull[a]), 1);
+            mbar_init(smem_u32(&tempty[a]), 2 * kPairEpiWarps);
+        }
         mbar_init(smem_u32(drain), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -948,32 +1020,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pdl_wait();
     pdl_release();
 
-    // (each role's code lies inside the branch that sets its registers: code after a
-    // join would have to do with the fewer)
-    if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairFewRegs));
-        if (warp == 0 && lane == 0) {
+    if (warp == 0) {
+        if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0, armed = 0, armed_parity = 0;
             bool ok = true;
             for (int64_t t = first; t < tiles && ok; t += step) {
                 const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
-                const int am = 2 * m + (int)rank, bn = 2 * n + (int)rank;  // this CTA's 128-row groups
-                for (int kb = 0; kb < p.nkb; ++kb) {
-                    if (!wait_bar(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag)) {
+                const int am = 2 * m + (int)rank;  // this CTA's 128-row group of A
+                const int sb = 3 * n / 2;         // the first 128-row group of the tile's rows of B
+                for (int kb = 0; kb < p.nkb; kb += kPerStage) {
+                    if (!wait_bar<true>(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag)) {
                         ok = false;
                         break;
                     }
                     armed |= 1u << stage;
                     armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-                    if (rank == 0) mbar_expect_tx(smem_u32(&full[stage]), (uint32_t)(2 * kStage2));
+                    const int blocks = min(kPerStage, p.nkb - kb);
+                    if (rank == 0)
+                        mbar_expect_tx(smem_u32(&full[stage]),
+                                       (uint32_t)(2 * (blocks * kCodes2 + ((kb & 3) == 0 ? kSf2 : 0))));
                     const uint32_t fb = in_even_cta(smem_u32(&full[stage]));
-                    tma_load_pair(smem_u32(sA + stage * kCodeTile), &tmA, kb * kBlock, am * 128, fb);
-                    tma_load_pair(smem_u32(sB + stage * kCodeTile), &tmB, kb * kBlock, bn * 128, fb);
-                    uint8_t* sf = sSf + stage * kSf2;
-                    tma_load_pair(smem_u32(sf), &tmSA, 0, am * groups + (kb >> 2), fb);
-                    tma_load_pair(smem_u32(sf + kAtomBytes), &tmSB, 0, 2 * n * groups + (kb >> 2), fb);
-                    tma_load_pair(smem_u32(sf + 2 * kAtomBytes), &tmSB, 0, (2 * n + 1) * groups + (kb >> 2), fb);
+                    for (int i = 0; i < blocks; ++i) {
+                        const int at = stage * kPerStage + i;
+                        tma_load_pair(smem_u32(sA + at * kCodeTile), &tmA, (kb + i) * kBlock, am * 128, fb);
+                        tma_load_pair(smem_u32(sB + at * kCodeTileB2), &tmB, (kb + i) * kBlock,
+                                      n * kPairN + (int)rank * (kPairN / 2), fb);
+                    }
+                    if ((kb & 3) == 0) {
+                        uint8_t* sf = sSf + stage * kSf2;
+                        tma_load_pair(smem_u32(sf), &tmSA, 0, am * groups + (kb >> 2), fb);
+                        tma_load_pair(smem_u32(sf + kAtomBytes), &tmSB, 0, sb * groups + (kb >> 2), fb);
+                        tma_load_pair(smem_u32(sf + 2 * kAtomBytes), &tmSB, 0, (sb + 1) * groups + (kb >> 2), fb);
+                    }
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
@@ -985,45 +1064,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (!ok && rank == 0)
                 for (int s = 0; s < S; ++s)
                     if (armed & (1u << s)) mbar_drain(smem_u32(&full[s]), (armed_parity >> s) & 1u, drain_limit);
-        } else if (warp == 1 && lane == 0 && rank == 0) {
-            int stage = 0;
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            int stage = 0, slot = S - 1;
             uint32_t phase = 0, span = 0;  // spans issued
             bool ok = true;
+            const uint64_t desc0 = smem_desc(0u, 2ull, 1024u);
+            const uint32_t a_base = smem_u32(sA) >> 4, b_base = smem_u32(sB) >> 4;
             for (int64_t t = first; t < tiles && ok; t += step) {
-                for (int kb = 0; kb < p.nkb; ++kb) {
-                    if (kb % kSpan == 0 && span > 0 &&
-                        !wait_bar(smem_u32(shared), (span - 1) & 1u, p.wait_limit, p.status, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!wait_bar(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag)) {
+                const int n = (int)(t % p.n_tiles);
+                for (int kb = 0; kb < p.nkb; kb += kPerStage) {
+                    if (kb % kSpan == 0)
+                        ok = wait_bar<true>(smem_u32(&tempty[span & 1u]), ((span >> 1) & 1u) ^ 1u, p.wait_limit,
+                                            p.status, abort_flag);
+                    ok = ok && wait_bar<true>(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sf = tmem_base + (uint32_t)(kSfBase2 + stage * kSfCols2);
+                    if ((kb & 3) == 0 && ++slot == S) slot = 0;
+                    const uint32_t sf = tmem_base + (uint32_t)(kSfBase2 + slot * kSfCols2);
+                    const uint32_t sfb = sf + 4 + 2 * (n & 1);
                     const uint32_t ssf = smem_u32(sSf + stage * kSf2);
+                    const uint32_t acc = tmem_base + (span & 1u) * kPairN;
+                    const int blocks = min(kPerStage, p.nkb - kb);
+                    const bool last = kb % kSpan + blocks == kSpan || kb + blocks == p.nkb;
+                    if (elect_one()) {
+                        if ((kb & 3) == 0) {
 #pragma unroll
-                    for (int q = 0; q < 3; ++q) copy_exponents<2>(sf + 4 * q, ssf + q * kAtomBytes);
-                    const uint32_t a0 = smem_u32(sA + stage * kCodeTile), b0 = smem_u32(sB + stage * kCodeTile);
-                    const uint32_t idesc = mm_idesc(256, 256, (uint32_t)(kb & 3));
+                            for (int q = 0; q < 3; ++q) copy_exponents<2>(sf + 4 * q, ssf + q * kAtomBytes);
+                        }
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_block8<2>(tmem_base + (span & 1u) * kAcc2, smem_desc(a0 + kk * 32, 2ull, 1024u),
-                                       smem_desc(b0 + kk * 32, 2ull, 1024u), idesc, sf, sf + 4,
-                                       (uint32_t)((kb % kSpan) | kk));
-                    commit_both(smem_u32(&empty[stage]));
+                        for (int i = 0; i < kPerStage; ++i) {
+                            if (i < blocks) {
+                                const int at = stage * kPerStage + i;
+                                const uint64_t ad = desc0 | (a_base + at * (kCodeTile >> 4));
+                                const uint64_t bd = desc0 | (b_base + at * (kCodeTileB2 >> 4));
+                                const uint32_t idesc = mm_idesc(256, kPairN, (uint32_t)((kb + i) & 3));
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    umma_block8<2>(acc, ad + 2 * kk, bd + 2 * kk, idesc, sf, sfb,
+                                                   (uint32_t)((kb % kSpan) | i | kk));
+                            }
+                        }
+                        commit_both(smem_u32(&empty[stage]));
+                        if (last) commit_both(smem_u32(&tfull[span & 1u]));
+                    }
+                    __syncwarp();
+                    if (last) ++span;
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
                     }
-                    if (kb % kSpan == kSpan - 1 || kb == p.nkb - 1) {
-                        commit_both(smem_u32(tfull));
-                        ++span;
-                    }
                 }
             }
-            if (!ok) {
+            if (!ok && elect_one()) {
                 asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                                  smem_u32(drain))
                              : "memory");
@@ -1031,44 +1128,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairEpiRegs));
-        const int ew = warp - 4;
-        const int q = warp & 3, half = ew >> 2;
+        const int ew = warp - 2;
+        const int q = warp & 3, third = ew >> 2;
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
         uint8_t* buf = turn + ew * 32 * 128;
-        const uint32_t shared_bar = in_even_cta(smem_u32(shared));
         uint32_t span = 0;
         bool ok = true;
         for (int64_t t = first; t < tiles && ok; t += step) {
             const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
             const int64_t row0 = (int64_t)m * 256 + rank * 128 + 32 * q;
-            const int64_t col0 = (int64_t)n * 256 + half * 128;
-            uint32_t sum[4][32];  // columns col0 + 32 ((i + 2 half) % 4)
+            const int64_t col0 = (int64_t)n * kPairN + third * 64;
+            uint32_t sum[2][32];
             clear_sums(sum);
             for (int kb = 0; kb < p.nkb; kb += kSpan) {
-                if (!__all_sync(0xFFFFFFFFu,
-                                wait_bar(smem_u32(tfull), span & 1u, p.wait_limit, p.status, abort_flag))) {
+                const uint32_t acc = span & 1u;
+                if (!__all_sync(0xFFFFFFFFu, wait_bar<true>(smem_u32(&tfull[acc]), (span >> 1) & 1u, p.wait_limit,
+                                                            p.status, abort_flag))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t tbase = tmem_base + lane_base + (span & 1u) * kAcc2 + (uint32_t)(half * 128);
+                const uint32_t tbase = tmem_base + lane_base + acc * kPairN + (uint32_t)(third * 64);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    add_columns(tbase + 32 * ((i + 2 * half) & 3), sum[i]);
-                    if (i == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(shared_bar)
-                                         : "memory");
-                    }
-                }
+                for (int i = 0; i < 2; ++i) add_columns(tbase + 32 * i, sum[i]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_remote(in_even_cta(smem_u32(&tempty[acc])));
                 ++span;
             }
             if (!ok) break;
-            store_rows<OB, 4>(sum, 2 * half, buf, lane, row0, col0, p);
+            if (row0 >= p.m_rows) continue;
+            if (p.vec_ok && col0 + 64 <= p.n_rows) {
+                if (OB == 4) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) store_tma(sum[i], buf, lane, (int)row0, (int)col0 + 32 * i, &tmOut);
+                } else {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        w[e] = pack_out(sum[e >> 4][2 * (e & 15)], sum[e >> 4][2 * (e & 15) + 1], p.bf16);
+                    store_tma(w, buf, lane, (int)row0, (int)col0, &tmOut);
+                }
+            } else {  // (a TMA store would fill the last 16 bytes of a row)
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                store_rows<OB, 2>(sum, buf, lane, row0, col0, p);
+            }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     tc_fence_before();
