@@ -309,6 +309,13 @@ class Block8:
         self.view = em_block8_t(self.codes.data_ptr(), self.scales.data_ptr(), self.claims.data_ptr(),
                                 self.status.data_ptr(), self.rows, self.d)
         self._ref = ctypes.byref(self.view)
+        self._index = -1 if self.device.index is None else self.device.index
+        self._types = {torch.float32: EM_DTYPE_F32, torch.bfloat16: EM_DTYPE_BF16, torch.float16: EM_DTYPE_F16}
+        self._int64 = torch.int64
+        # the current stream's handle alone (torch.cuda.current_stream makes an object of
+        # it, 2 us of a call of 7)
+        self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
 
     @property
     def shape(self):
@@ -316,37 +323,38 @@ class Block8:
 
     def _stream(self, stream):
         if stream is None:
-            import torch
-
-            stream = torch.cuda.current_stream(self.device)
+            return self._current(self._index)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
+    def _here(self, t, name):
+        if t.get_device() != self._index or (self._index < 0 and t.device != self.device):
+            raise ValueError(f"{name} is on {t.device}, the matrix on {self.device}")
+
     def _matrix(self, t, cols, name):
-        """Type code and element strides of a 2-D tensor of `cols` columns on this device."""
-        dtype = _DTYPES.get(str(t.dtype))
+        """Rows, type code and element strides of a 2-D tensor of `cols` columns on this device."""
+        dtype = self._types.get(t.dtype)
         if dtype is None:
             raise TypeError(f"{name} must be float32, bfloat16 or float16, not {t.dtype}")
-        if t.dim() != 2 or t.shape[1] != cols:
-            raise ValueError(f"{name} must be 2-D with {cols} columns, not {tuple(t.shape)}")
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the matrix on {self.device}")
+        shape = t.shape
+        if len(shape) != 2 or shape[1] != cols:
+            raise ValueError(f"{name} must be 2-D with {cols} columns, not {tuple(shape)}")
+        self._here(t, name)
         rs, cs = t.stride()
         # a dimension of one element has no stride of its own
         if cols == 1:
             cs = 1
-        if t.shape[0] == 1 and cs != 1:
+        if shape[0] == 1 and cs != 1:
             rs = 1
-        return dtype, rs, cs
+        return shape[0], dtype, rs, cs
 
     def _slots(self, slots, n, first):
         if slots is None:
             return None
-        if str(slots.dtype) != "torch.int64" or slots.dim() != 1 or not slots.is_contiguous():
+        if slots.dtype != self._int64 or slots.dim() != 1 or not slots.is_contiguous():
             raise ValueError("slots must be a contiguous 1-D int64 tensor")
         if len(slots) != n:
             raise ValueError(f"{len(slots)} slots for {n} rows")
-        if slots.device != self.device:
-            raise ValueError(f"slots are on {slots.device}, the matrix on {self.device}")
+        self._here(slots, "slots")
         if first:
             raise ValueError("first must be 0 with slots")
         return slots.data_ptr() if n else None
@@ -354,42 +362,41 @@ class Block8:
     def write(self, X, first=0, slots=None, stream=None):
         """Quantises X (n x d; row- or column-contiguous) into rows first, first + 1, ...,
         or into rows slots[i] (-1: not written; the last of equal slots stays)."""
-        dtype, rs, cs = self._matrix(X, self.d, "X")
-        n = X.shape[0]
-        slots = self._slots(slots, n, first)
-        check(em_block8_write(self._ref, X.data_ptr(), dtype, n, rs, cs, int(first), slots, self._stream(stream)),
-              "em_block8_write")
+        n, dtype, rs, cs = self._matrix(X, self.d, "X")
+        rc = em_block8_write(self._ref, X.data_ptr(), dtype, n, rs, cs, first, self._slots(slots, n, first),
+                             self._stream(stream))
+        if rc:
+            check(rc, "em_block8_write")
 
     def read(self, out, first=0, slots=None, stream=None):
         """Reads out.shape[0] rows from `first` on, or rows slots[i] (-1: zeros), into out."""
-        dtype, rs, cs = self._matrix(out, self.d, "out")
-        n = out.shape[0]
+        n, dtype, rs, cs = self._matrix(out, self.d, "out")
         if cs != 1 and n:
             raise ValueError("the rows of out must be contiguous")
-        slots = self._slots(slots, n, first)
-        check(em_block8_read(self._ref, int(first), slots, n, out.data_ptr(), dtype, rs if n > 1 else self.d,
-                             self._stream(stream)), "em_block8_read")
+        rc = em_block8_read(self._ref, first, self._slots(slots, n, first), n, out.data_ptr(), dtype,
+                            rs if n > 1 else self.d, self._stream(stream))
+        if rc:
+            check(rc, "em_block8_read")
         return out
 
     def matmul(self, other, out, stream=None):
         """out[i, j] = row i of this matrix . row j of `other`, for out's shape."""
-        dtype, rs, cs = self._matrix(out, out.shape[-1], "out")
+        nb = out.shape[-1]
+        na, dtype, rs, cs = self._matrix(out, nb, "out")
         if other.device != self.device:
             raise ValueError(f"the other matrix is on {other.device}, this one on {self.device}")
-        na, nb = out.shape
         if cs != 1 and na and nb:
             raise ValueError("the rows of out must be contiguous")
-        check(em_block8_matmul(self._ref, na, other._ref, nb, out.data_ptr(), dtype, rs if na > 1 else nb,
-                               self._stream(stream)), "em_block8_matmul")
+        rc = em_block8_matmul(self._ref, na, other._ref, nb, out.data_ptr(), dtype, rs if na > 1 else nb,
+                              self._stream(stream))
+        if rc:
+            check(rc, "em_block8_matmul")
         return out
 
     def check(self, stream=None):
         """Waits for the stream; raises EmeansError for a device-side error (a slot
         outside the matrix) since the last check."""
         check(em_block8_check(self._ref, self._stream(stream)), "em_block8_check")
-
-
-_DTYPES = {"torch.float32": EM_DTYPE_F32, "torch.bfloat16": EM_DTYPE_BF16, "torch.float16": EM_DTYPE_F16}
 
 
 def exchange_dp_id(group=None):

@@ -117,10 +117,12 @@ int b8_device(int dev, DeviceFacts* out) {
         if (major != 10 || minor != 0) return fail(EM_E_NODEVICE, "this library is built for sm_100a (B200)");
         CK(cudaDeviceGetAttribute(&f.sms, cudaDevAttrMultiProcessorCount, dev));
         CK(cudaDeviceGetAttribute(&f.clock_khz, cudaDevAttrClockRate, dev));
-        if (!b8_smem_attribute(b8::k_block8_matmul<4, false>, b8::kSmem1) ||
-            !b8_smem_attribute(b8::k_block8_matmul<2, false>, b8::kSmem1) ||
-            !b8_smem_attribute(b8::k_block8_matmul<4, true>, b8::kSmem1) ||
-            !b8_smem_attribute(b8::k_block8_matmul<2, true>, b8::kSmem1) ||
+        if (!b8_smem_attribute(b8::k_block8_matmul<128, 4, false>, b8::MmCfg<128, false>::kSmem) ||
+            !b8_smem_attribute(b8::k_block8_matmul<128, 2, false>, b8::MmCfg<128, false>::kSmem) ||
+            !b8_smem_attribute(b8::k_block8_matmul<128, 4, true>, b8::MmCfg<128, true>::kSmem) ||
+            !b8_smem_attribute(b8::k_block8_matmul<128, 2, true>, b8::MmCfg<128, true>::kSmem) ||
+            !b8_smem_attribute(b8::k_block8_matmul<32, 4, true>, b8::MmCfg<32, true>::kSmem) ||
+            !b8_smem_attribute(b8::k_block8_matmul<32, 2, true>, b8::MmCfg<32, true>::kSmem) ||
             !b8_smem_attribute(b8::k_block8_matmul_pair<4>, b8::kSmem2) ||
             !b8_smem_attribute(b8::k_block8_matmul_pair<2>, b8::kSmem2)) {
             cudaGetLastError();
@@ -224,6 +226,16 @@ int b8_out_map(CUtensorMap* tm, const b8::MmArgs& p, size_t esz) {
     return EM_OK;
 }
 
+template <int BN, bool SWAP>
+int b8_launch_single(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmSA, const CUtensorMap& tmSB,
+                     const b8::MmArgs& p, size_t esz, int sms, cudaStream_t st) {
+    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+    CK(launch_k(true, esz == 4 ? b8::k_block8_matmul<BN, 4, SWAP> : b8::k_block8_matmul<BN, 2, SWAP>,
+                dim3((unsigned)std::min<int64_t>(tiles, sms)), dim3(b8::kMmThreads), b8::MmCfg<BN, SWAP>::kSmem, st, tmA,
+                tmB, tmSA, tmSB, p));
+    return EM_OK;
+}
+
 // A product with the rows of `a` on the tiles' M side; `swap`: they are the output's columns.
 int b8_launch_matmul(const em_block8_t* a, int64_t na, const em_block8_t* b, int64_t nb, bool swap, b8::MmArgs p,
                      size_t esz, int sms, cudaStream_t st) {
@@ -234,9 +246,11 @@ int b8_launch_matmul(const em_block8_t* a, int64_t na, const em_block8_t* b, int
     const int64_t t2 = ((na + 255) / 256) * ((nb + b8::kPairN - 1) / b8::kPairN);
     const int64_t pairs = std::max(sms / 2, 1);
     const bool pair = !swap && (t2 + pairs - 1) / pairs * 384 <= (t1 + sms - 1) / sms * 400;
+    const bool narrow = swap && nb <= 32;
+    const int box_b = pair ? b8::kPairN / 2 : narrow ? 32 : 128;
     CUtensorMap tmA, tmB, tmSA, tmSB;
     CKR(make_tmap8(&tmA, a->codes, a->rows, (int)a->d, (int)b8_pitch(a->d), 128));
-    CKR(make_tmap8(&tmB, b->codes, b->rows, (int)b->d, (int)b8_pitch(b->d), pair ? b8::kPairN / 2 : 128));
+    CKR(make_tmap8(&tmB, b->codes, b->rows, (int)b->d, (int)b8_pitch(b->d), box_b));
     CKR(b8_scale_map(&tmSA, a));
     CKR(b8_scale_map(&tmSB, b));
     p.m_rows = na;
@@ -255,12 +269,10 @@ int b8_launch_matmul(const em_block8_t* a, int64_t na, const em_block8_t* b, int
         return EM_OK;
     }
     p.m_tiles = (int)((na + 127) / 128);
-    p.n_tiles = (int)((nb + 127) / 128);
-    auto* kernel = esz == 4 ? (swap ? b8::k_block8_matmul<4, true> : b8::k_block8_matmul<4, false>)
-                            : (swap ? b8::k_block8_matmul<2, true> : b8::k_block8_matmul<2, false>);
-    CK(launch_k(true, kernel, dim3((unsigned)std::min<int64_t>(t1, sms)), dim3(b8::kMmThreads), b8::kSmem1, st, tmA, tmB,
-                tmSA, tmSB, p));
-    return EM_OK;
+    p.n_tiles = (int)((nb + box_b - 1) / box_b);
+    if (narrow) return b8_launch_single<32, true>(tmA, tmB, tmSA, tmSB, p, esz, sms, st);
+    if (swap) return b8_launch_single<128, true>(tmA, tmB, tmSA, tmSB, p, esz, sms, st);
+    return b8_launch_single<128, false>(tmA, tmB, tmSA, tmSB, p, esz, sms, st);
 }
 
 }  // namespace

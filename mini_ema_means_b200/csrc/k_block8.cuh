@@ -449,10 +449,10 @@ __global__ void __launch_bounds__(256)
 // Roles of a CTA's 10 warps:
 //   warp 0     one thread loads 128-byte-wide tiles of codes (TMA, 128-byte swizzle)
 //              and the exponents of their rows into a ring of stages
-//   warp 1     one thread issues the MMAs and, every fourth block, copies the exponents
-//              of four blocks to tensor memory. They go round as many sets of columns
-//              there as the ring has stages: a set's last user is at least that many
-//              blocks back, and the wait for this block's stage was a wait for it
+//   warp 1     one thread issues the MMAs and, at every fourth block of a row, copies the
+//              exponents of four blocks to tensor memory. They go round as many sets of
+//              columns there as the ring has blocks: a set's last user is at least that
+//              many blocks back, and the wait for this block's stage was a wait for it
 //   warps 2-9  epilogue: two groups of four warps (one per TMEM lane quadrant) take
 //              the left and right half of a tile's columns
 
@@ -669,38 +669,53 @@ __device__ __forceinline__ void store_rows(const uint32_t (&sum)[NS][32], uint8_
     }
 }
 
-// ---- one CTA per 128 x 128 tile: few tiles, or few rows on one side
+// ---- one CTA per 128 x BN tile: few tiles, or few rows on one side
 //
 // SWAP: the M operand is the one whose rows are the output's columns (few output
 // rows): a lane holds one output column and a warp stores 32 neighbours at once.
+// With few rows the product streams the long operand once, and what counts is bytes in
+// flight: BN = 32 keeps the stages small and lets two groups of four epilogue warps
+// take tiles in turn, four accumulators ahead.
+//
+// The blocks of all of a CTA's tiles form one sequence, PER of them to a stage: a
+// barrier round trip serves PER blocks whatever the rows' length.
 
-constexpr int kBN1 = 128;
-constexpr int kStage1 = 2 * kCodeTile + 2 * kAtomBytes;
-constexpr int kFixed1 = 1024 + 256 + kTurnBytes;
-constexpr int kStages1 = 5;
-constexpr int kSmem1 = kFixed1 + kStages1 * kStage1;
-constexpr int kSfCols1 = 8;
-static_assert(kSmem1 <= 227 * 1024 && 2 * kBN1 + kStages1 * kSfCols1 <= 512, "shared or tensor memory");
+template <int BN, bool SWAP>
+struct MmCfg {
+    static constexpr int kPer = SWAP ? 2 : 1;
+    static constexpr int kStages = !SWAP ? 5 : BN == 32 ? 5 : 3;
+    static constexpr int kBTile = BN * 128;
+    static constexpr int kCodes = kCodeTile + kBTile;  // codes of one block
+    static constexpr int kSf = 2 * kAtomBytes;
+    static constexpr bool kTurns = SWAP && BN == 32;   // the epilogue's halves take tiles in turn
+    static constexpr int kAcc = kTurns ? 4 : 2;
+    static constexpr int kSmem = 1024 + 256 + (SWAP ? 0 : kTurnBytes) + kStages * kPer * (kCodes + kSf);
+    static constexpr int kSfCols = 8;
+    static constexpr int kSfSlots = kStages * kPer;
+    static constexpr int kSfBase = kAcc * BN;
+    static_assert(kSmem <= 227 * 1024 && kSfBase + kSfSlots * kSfCols <= 512, "shared or tensor memory");
+};
 
-template <int OB, bool SWAP>
+template <int BN, int OB, bool SWAP>
 __global__ void __launch_bounds__(kMmThreads, 1)
     k_block8_matmul(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, const MmArgs p) {
     using namespace tc;
-    constexpr int S = kStages1;
+    using C = MmCfg<BN, SWAP>;
+    constexpr int S = C::kStages, PER = C::kPer, ACC = C::kAcc;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
-    uint8_t* sB = sA + S * kCodeTile;
-    uint8_t* turn = sB + S * kCodeTile;
-    uint8_t* sSf = turn + kTurnBytes;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sSf + S * 2 * kAtomBytes);
+    uint8_t* sB = sA + S * PER * kCodeTile;
+    uint8_t* turn = sB + S * PER * C::kBTile;
+    uint8_t* sSf = turn + (SWAP ? 0 : kTurnBytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sSf + S * PER * C::kSf);
     uint64_t* full = bars;
     uint64_t* empty = bars + S;
     uint64_t* tfull = bars + 2 * S;
-    uint64_t* tempty = bars + 2 * S + 2;
-    uint64_t* drain = bars + 2 * S + 4;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+    uint64_t* tempty = tfull + ACC;
+    uint64_t* drain = tempty + ACC;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -710,12 +725,12 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&full[s]), PER);
             mbar_init(smem_u32(&empty[s]), 1);
         }
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < ACC; ++a) {
             mbar_init(smem_u32(&tfull[a]), 1);
-            mbar_init(smem_u32(&tempty[a]), kMmEpi);
+            mbar_init(smem_u32(&tempty[a]), C::kTurns ? 4 : 8);
         }
         mbar_init(smem_u32(drain), 1);
         *abort_flag = 0;
@@ -736,135 +751,160 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     pdl_release();
 
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, armed = 0, armed_parity = 0;
-            bool ok = true;
-            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
-                for (int kb = 0; kb < p.nkb; ++kb) {
-                    if (!wait_bar(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag)) {
+        int stage = 0, part = 0;  // the next block's stage, and its place there
+        uint32_t phase = 0, armed = 0, armed_parity = 0;
+        bool ok = true;
+        for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
+            for (int kb = 0; kb < p.nkb; ++kb) {
+                if (part == 0) {
+                    ok = wait_bar(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t fb = smem_u32(&full[stage]);
                     armed |= 1u << stage;
                     armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-                    mbar_expect_tx(fb, (uint32_t)((kb & 3) == 0 ? kStage1 : 2 * kCodeTile));
-                    tma_load_2d(smem_u32(sA + stage * kCodeTile), &tmA, kb * kBlock, m * 128, fb);
-                    tma_load_2d(smem_u32(sB + stage * kCodeTile), &tmB, kb * kBlock, n * kBN1, fb);
+                }
+                if (elect_one()) {
+                    const uint32_t fb = smem_u32(&full[stage]);
+                    const int at = stage * PER + part;
+                    mbar_expect_tx(fb, (uint32_t)(C::kCodes + ((kb & 3) == 0 ? C::kSf : 0)));
+                    tma_load_2d(smem_u32(sA + at * kCodeTile), &tmA, kb * kBlock, m * 128, fb);
+                    tma_load_2d(smem_u32(sB + at * C::kBTile), &tmB, kb * kBlock, n * BN, fb);
                     if ((kb & 3) == 0) {
-                        uint8_t* sf = sSf + stage * 2 * kAtomBytes;
+                        uint8_t* sf = sSf + at * C::kSf;
                         tma_load_2d(smem_u32(sf), &tmSA, 0, m * groups + (kb >> 2), fb);
                         tma_load_2d(smem_u32(sf + kAtomBytes), &tmSB, 0, n * groups + (kb >> 2), fb);
                     }
+                }
+                __syncwarp();
+                if (++part == PER) {
+                    part = 0;
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            if (!ok)
-                for (int s = 0; s < S; ++s)
-                    if (armed & (1u << s)) mbar_drain(smem_u32(&full[s]), (armed_parity >> s) & 1u, drain_limit);
         }
+        if (part > 0 && elect_one())  // the last stage's missing blocks
+            for (; part < PER; ++part) mbar_arrive(smem_u32(&full[stage]));
+        __syncwarp();
+        if (!ok && lane == 0)
+            for (int s = 0; s < S; ++s)
+                if (armed & (1u << s)) mbar_drain(smem_u32(&full[s]), (armed_parity >> s) & 1u, drain_limit);
     } else if (warp == 1) {
-        if (lane == 0) {
-            int stage = 0, acc = 0, slot = S - 1;
-            uint32_t phase = 0, acc_phase = 0;
-            bool ok = true;
-            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                for (int kb = 0; kb < p.nkb; ++kb) {
-                    if (kb % kSpan == 0 &&
-                        !wait_bar(smem_u32(&tempty[acc]), acc_phase ^ 1u, p.wait_limit, p.status, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!wait_bar(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if ((kb & 3) == 0 && ++slot == S) slot = 0;
-                    const uint32_t sf = tmem_base + (uint32_t)(2 * kBN1 + slot * kSfCols1);
+        int stage = 0, part = 0, acc = 0, slot = C::kSfSlots - 1;
+        uint32_t phase = 0, acc_phase = 0;
+        bool ok = true;
+        const uint64_t desc0 = smem_desc(0u, 2ull, 1024u);
+        const uint32_t a_base = smem_u32(sA) >> 4, b_base = smem_u32(sB) >> 4;
+        for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int kb = 0; kb < p.nkb; ++kb) {
+                if (kb % kSpan == 0)
+                    ok = wait_bar(smem_u32(&tempty[acc]), acc_phase ^ 1u, p.wait_limit, p.status, abort_flag);
+                if (part == 0)
+                    ok = ok && wait_bar(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if ((kb & 3) == 0 && ++slot == C::kSfSlots) slot = 0;
+                const int at = stage * PER + part;
+                const uint32_t sf = tmem_base + (uint32_t)(C::kSfBase + slot * C::kSfCols);
+                const uint32_t ssf = smem_u32(sSf + at * C::kSf);
+                const uint64_t ad = desc0 | (a_base + at * (kCodeTile >> 4));
+                const uint64_t bd = desc0 | (b_base + at * (C::kBTile >> 4));
+                const uint32_t idesc = mm_idesc(128, BN, (uint32_t)(kb & 3));
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+                const bool last = kb % kSpan == kSpan - 1 || kb == p.nkb - 1;
+                if (elect_one()) {
                     if ((kb & 3) == 0) {
-                        const uint32_t ssf = smem_u32(sSf + stage * 2 * kAtomBytes);
                         copy_exponents<1>(sf, ssf);
                         copy_exponents<1>(sf + 4, ssf + kAtomBytes);
                     }
-                    const uint32_t a0 = smem_u32(sA + stage * kCodeTile), b0 = smem_u32(sB + stage * kCodeTile);
-                    const uint32_t idesc = mm_idesc(128, kBN1, (uint32_t)(kb & 3));
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_block8<1>(tmem_base + (uint32_t)(acc * kBN1), smem_desc(a0 + kk * 32, 2ull, 1024u),
-                                       smem_desc(b0 + kk * 32, 2ull, 1024u), idesc, sf, sf + 4,
+                        umma_block8<1>(d_tmem, ad + 2 * kk, bd + 2 * kk, idesc, sf, sf + 4,
                                        (uint32_t)((kb % kSpan) | kk));
-                    umma_commit(smem_u32(&empty[stage]));
+                    if (part == PER - 1) umma_commit(smem_u32(&empty[stage]));
+                    if (last) umma_commit(smem_u32(&tfull[acc]));
+                }
+                __syncwarp();
+                if (last && ++acc == ACC) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+                if (++part == PER) {
+                    part = 0;
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
                     }
-                    if (kb % kSpan == kSpan - 1 || kb == p.nkb - 1) {
-                        umma_commit(smem_u32(&tfull[acc]));
-                        acc ^= 1;
-                        if (acc == 0) acc_phase ^= 1u;
-                    }
                 }
             }
-            if (!ok) {
-                umma_commit(smem_u32(drain));
-                mbar_drain(smem_u32(drain), 0u, drain_limit);
-            }
+        }
+        if (!ok && elect_one()) {
+            umma_commit(smem_u32(drain));
+            mbar_drain(smem_u32(drain), 0u, drain_limit);
         }
     } else {
         const int ew = warp - 2;
         const int q = warp & 3, half = ew >> 2;
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+        constexpr int kCols = C::kTurns ? BN : BN / 2;  // columns a warp takes
+        constexpr int NS = kCols / 32;
         uint8_t* buf = turn + ew * 32 * 128;
-        int acc = 0;
-        uint32_t acc_phase = 0;
+        const int spans = (p.nkb + kSpan - 1) / kSpan;
+        int64_t span = C::kTurns ? (int64_t)half * spans : 0;  // spans of the CTA before this tile's
         bool ok = true;
-        for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int64_t t = blockIdx.x + (C::kTurns ? (int64_t)half * gridDim.x : 0); t < tiles && ok;
+             t += (C::kTurns ? 2 : 1) * (int64_t)gridDim.x) {
             const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
             const int64_t row0 = (int64_t)m * 128 + 32 * q;
-            const int64_t col0 = (int64_t)n * kBN1 + half * (kBN1 / 2);
-            uint32_t sum[2][32];
+            const int64_t col0 = (int64_t)n * BN + (C::kTurns ? 0 : half * kCols);
+            uint32_t sum[NS][32];
             clear_sums(sum);
-            for (int kb = 0; kb < p.nkb; kb += kSpan) {
-                if (!__all_sync(0xFFFFFFFFu,
-                                wait_bar(smem_u32(&tfull[acc]), acc_phase, p.wait_limit, p.status, abort_flag))) {
+            for (int s = 0; s < spans; ++s) {
+                const int acc = (int)(span % ACC);
+                if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&tfull[acc]), (uint32_t)(span / ACC) & 1u, p.wait_limit,
+                                                      p.status, abort_flag))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t tbase = tmem_base + lane_base + (uint32_t)(acc * kBN1 + half * (kBN1 / 2));
+                const uint32_t tbase = tmem_base + lane_base + (uint32_t)(acc * BN + (C::kTurns ? 0 : half * kCols));
 #pragma unroll
-                for (int i = 0; i < 2; ++i) add_columns(tbase + 32 * i, sum[i]);
+                for (int i = 0; i < NS; ++i) add_columns(tbase + 32 * i, sum[i]);
                 tc_fence_before();
-                mbar_arrive(smem_u32(&tempty[acc]));
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1u;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&tempty[acc]));
+                ++span;
             }
+            if (C::kTurns) span += spans;  // the other half's tile
             if (!ok) break;
             if (SWAP) {
                 const int64_t j = row0 + lane;  // output column
+                const int rows = (int)min(p.n_rows - col0, (int64_t)kCols);
+                uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + (col0 * p.ldo + j) * OB;
                 if (j < p.m_rows) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < NS; ++i)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            const int64_t r = col0 + 32 * i + e;  // output row
-                            if (r < p.n_rows) {
+                            if (32 * i + e < rows) {
                                 if (OB == 4)
-                                    reinterpret_cast<uint32_t*>(p.out)[r * p.ldo + j] = sum[i][e];
+                                    *reinterpret_cast<uint32_t*>(dst) = sum[i][e];
                                 else
-                                    reinterpret_cast<uint16_t*>(p.out)[r * p.ldo + j] =
-                                        (uint16_t)pack_out(sum[i][e], 0u, p.bf16);
+                                    *reinterpret_cast<uint16_t*>(dst) = (uint16_t)pack_out(sum[i][e], 0u, p.bf16);
                             }
+                            dst += p.ldo * OB;
                         }
                 }
             } else {
-                store_rows<OB, 2>(sum, buf, lane, row0, col0, p);
+                store_rows<OB, NS>(sum, buf, lane, row0, col0, p);
             }
         }
     }
@@ -905,11 +945,11 @@ constexpr int kTurnBytes2 = kPairEpiWarps * 32 * 128;
 constexpr int kCodeTileB2 = kPairN / 2 * 128;
 constexpr int kSf2 = 3 * kAtomBytes;
 constexpr int kCodes2 = kCodeTile + kCodeTileB2;  // codes of one block
-constexpr int kSmem2 = 1024 + 256 + kTurnBytes2 + kStages2 * (kPerStage * kCodes2 + kSf2);
+constexpr int kSmem2 = 1024 + 256 + kTurnBytes2 + kStages2 * kPerStage * (kCodes2 + kSf2);
+constexpr int kSfSlots2 = kStages2 * kPerStage;
 constexpr int kSfCols2 = 12;
 constexpr int kSfBase2 = 2 * kPairN;
-static_assert(kSmem2 <= 227 * 1024 && kSfBase2 + kStages2 * kSfCols2 <= 512, "shared or tensor memory");
-static_assert(4 % kPerStage == 0 && kSpan % 4 == 0, "a stage lies within a group of exponents, a group within a span");
+static_assert(kSmem2 <= 227 * 1024 && kSfBase2 + kSfSlots2 * kSfCols2 <= 512, "shared or tensor memory");
 
 // The address of `addr` (this CTA's shared memory) in the pair's even CTA.
 __device__ __forceinline__ uint32_t in_even_cta(uint32_t addr) {
@@ -975,7 +1015,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     uint8_t* sB = sA + S * kPerStage * kCodeTile;
     uint8_t* turn = sB + S * kPerStage * kCodeTileB2;
     uint8_t* sSf = turn + kTurnBytes2;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sSf + S * kSf2);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sSf + S * kPerStage * kSf2);
     uint64_t* full = bars;            // (even CTA) both CTAs' loads of a stage
     uint64_t* empty = bars + S;       // (each CTA) the MMAs are done with a stage
     uint64_t* tfull = bars + 2 * S;   // (each CTA) an accumulator is complete
@@ -994,7 +1034,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&full[s]), kPerStage);
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -1021,102 +1061,106 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pdl_release();
 
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, armed = 0, armed_parity = 0;
-            bool ok = true;
-            for (int64_t t = first; t < tiles && ok; t += step) {
-                const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
-                const int am = 2 * m + (int)rank;  // this CTA's 128-row group of A
-                const int sb = 3 * n / 2;         // the first 128-row group of the tile's rows of B
-                for (int kb = 0; kb < p.nkb; kb += kPerStage) {
-                    if (!wait_bar<true>(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag)) {
+        int stage = 0, part = 0;
+        uint32_t phase = 0, armed = 0, armed_parity = 0;
+        bool ok = true;
+        for (int64_t t = first; t < tiles && ok; t += step) {
+            const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
+            const int am = 2 * m + (int)rank;  // this CTA's 128-row group of A
+            const int sb = 3 * n / 2;          // the first 128-row group of the tile's rows of B
+            for (int kb = 0; kb < p.nkb; ++kb) {
+                if (part == 0) {
+                    ok = wait_bar<true>(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) {
                         ok = false;
                         break;
                     }
                     armed |= 1u << stage;
                     armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-                    const int blocks = min(kPerStage, p.nkb - kb);
+                }
+                if (elect_one()) {
+                    const int at = stage * kPerStage + part;
                     if (rank == 0)
-                        mbar_expect_tx(smem_u32(&full[stage]),
-                                       (uint32_t)(2 * (blocks * kCodes2 + ((kb & 3) == 0 ? kSf2 : 0))));
+                        mbar_expect_tx(smem_u32(&full[stage]), (uint32_t)(2 * (kCodes2 + ((kb & 3) == 0 ? kSf2 : 0))));
                     const uint32_t fb = in_even_cta(smem_u32(&full[stage]));
-                    for (int i = 0; i < blocks; ++i) {
-                        const int at = stage * kPerStage + i;
-                        tma_load_pair(smem_u32(sA + at * kCodeTile), &tmA, (kb + i) * kBlock, am * 128, fb);
-                        tma_load_pair(smem_u32(sB + at * kCodeTileB2), &tmB, (kb + i) * kBlock,
-                                      n * kPairN + (int)rank * (kPairN / 2), fb);
-                    }
+                    tma_load_pair(smem_u32(sA + at * kCodeTile), &tmA, kb * kBlock, am * 128, fb);
+                    tma_load_pair(smem_u32(sB + at * kCodeTileB2), &tmB, kb * kBlock,
+                                  n * kPairN + (int)rank * (kPairN / 2), fb);
                     if ((kb & 3) == 0) {
-                        uint8_t* sf = sSf + stage * kSf2;
+                        uint8_t* sf = sSf + at * kSf2;
                         tma_load_pair(smem_u32(sf), &tmSA, 0, am * groups + (kb >> 2), fb);
                         tma_load_pair(smem_u32(sf + kAtomBytes), &tmSB, 0, sb * groups + (kb >> 2), fb);
                         tma_load_pair(smem_u32(sf + 2 * kAtomBytes), &tmSB, 0, (sb + 1) * groups + (kb >> 2), fb);
                     }
+                }
+                __syncwarp();
+                if (++part == kPerStage) {
+                    part = 0;
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            // (the even CTA's barriers stand for both CTAs' loads; neither CTA leaves
-            // before the other, see the end)
-            if (!ok && rank == 0)
-                for (int s = 0; s < S; ++s)
-                    if (armed & (1u << s)) mbar_drain(smem_u32(&full[s]), (armed_parity >> s) & 1u, drain_limit);
         }
+        if (part > 0 && rank == 0 && elect_one())  // the last stage's missing blocks
+            for (; part < kPerStage; ++part) mbar_arrive(smem_u32(&full[stage]));
+        __syncwarp();
+        // (the even CTA's barriers stand for both CTAs' loads; neither CTA leaves before
+        // the other, see the end)
+        if (!ok && rank == 0 && lane == 0)
+            for (int s = 0; s < S; ++s)
+                if (armed & (1u << s)) mbar_drain(smem_u32(&full[s]), (armed_parity >> s) & 1u, drain_limit);
     } else if (warp == 1) {
         if (rank == 0) {
-            int stage = 0, slot = S - 1;
+            int stage = 0, part = 0, slot = kSfSlots2 - 1;
             uint32_t phase = 0, span = 0;  // spans issued
             bool ok = true;
             const uint64_t desc0 = smem_desc(0u, 2ull, 1024u);
             const uint32_t a_base = smem_u32(sA) >> 4, b_base = smem_u32(sB) >> 4;
             for (int64_t t = first; t < tiles && ok; t += step) {
                 const int n = (int)(t % p.n_tiles);
-                for (int kb = 0; kb < p.nkb; kb += kPerStage) {
+                for (int kb = 0; kb < p.nkb; ++kb) {
                     if (kb % kSpan == 0)
                         ok = wait_bar<true>(smem_u32(&tempty[span & 1u]), ((span >> 1) & 1u) ^ 1u, p.wait_limit,
                                             p.status, abort_flag);
-                    ok = ok && wait_bar<true>(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag);
+                    if (part == 0)
+                        ok = ok && wait_bar<true>(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag);
                     if (!__all_sync(0xFFFFFFFFu, ok)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    if ((kb & 3) == 0 && ++slot == S) slot = 0;
+                    if ((kb & 3) == 0 && ++slot == kSfSlots2) slot = 0;
+                    const int at = stage * kPerStage + part;
                     const uint32_t sf = tmem_base + (uint32_t)(kSfBase2 + slot * kSfCols2);
                     const uint32_t sfb = sf + 4 + 2 * (n & 1);
-                    const uint32_t ssf = smem_u32(sSf + stage * kSf2);
+                    const uint32_t ssf = smem_u32(sSf + at * kSf2);
+                    const uint64_t ad = desc0 | (a_base + at * (kCodeTile >> 4));
+                    const uint64_t bd = desc0 | (b_base + at * (kCodeTileB2 >> 4));
+                    const uint32_t idesc = mm_idesc(256, kPairN, (uint32_t)(kb & 3));
                     const uint32_t acc = tmem_base + (span & 1u) * kPairN;
-                    const int blocks = min(kPerStage, p.nkb - kb);
-                    const bool last = kb % kSpan + blocks == kSpan || kb + blocks == p.nkb;
+                    const bool last = kb % kSpan == kSpan - 1 || kb == p.nkb - 1;
                     if (elect_one()) {
                         if ((kb & 3) == 0) {
 #pragma unroll
                             for (int q = 0; q < 3; ++q) copy_exponents<2>(sf + 4 * q, ssf + q * kAtomBytes);
                         }
 #pragma unroll
-                        for (int i = 0; i < kPerStage; ++i) {
-                            if (i < blocks) {
-                                const int at = stage * kPerStage + i;
-                                const uint64_t ad = desc0 | (a_base + at * (kCodeTile >> 4));
-                                const uint64_t bd = desc0 | (b_base + at * (kCodeTileB2 >> 4));
-                                const uint32_t idesc = mm_idesc(256, kPairN, (uint32_t)((kb + i) & 3));
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk)
-                                    umma_block8<2>(acc, ad + 2 * kk, bd + 2 * kk, idesc, sf, sfb,
-                                                   (uint32_t)((kb % kSpan) | i | kk));
-                            }
-                        }
-                        commit_both(smem_u32(&empty[stage]));
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_block8<2>(acc, ad + 2 * kk, bd + 2 * kk, idesc, sf, sfb,
+                                           (uint32_t)((kb % kSpan) | kk));
+                        if (part == kPerStage - 1) commit_both(smem_u32(&empty[stage]));
                         if (last) commit_both(smem_u32(&tfull[span & 1u]));
                     }
                     __syncwarp();
                     if (last) ++span;
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
+                    if (++part == kPerStage) {
+                        part = 0;
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
                 }
             }
