@@ -147,16 +147,16 @@ int b8_write(bool cols, const void* X_, int64_t n, int64_t ldx, const int64_t* s
     const int64_t nb = b8_blocks(m->d);
     const int d = (int)m->d, pitch = (int)b8_pitch(m->d);
     if (!cols) {
-        CK(launch_k(true, b8::k_block8_write<T>, dim3(b8_pair_grid(n, nb, sms)), dim3(256), 0, st, X, (int)n, d, ldx,
-                    b8::vector_width<T>(X, ldx), slots, first, claims, codes, scales, m->rows, pitch,
+        CK(launch_k(true, slots ? b8::k_block8_write<T, true> : b8::k_block8_write<T, false>,
+                    dim3(b8_pair_grid(n, nb, sms)), dim3(256), 0, st, X, (int)n, d, ldx, b8::vector_width<T>(X, ldx), slots,
+                    (int)first, claims, codes, scales, m->rows, pitch,
                     b8::FastDiv((uint32_t)nb), m->status));
         return EM_OK;
     }
-    const int64_t row_tiles = (n + b8::kColRows - 1) / b8::kColRows;
-    const int vec_ok = (uintptr_t)X % (2 * sizeof(T)) == 0 && ldx % 2 == 0;
+    const int64_t row_tiles = (n + b8::ColTile<T>::kRows - 1) / b8::ColTile<T>::kRows;
     const int grid = (int)std::min<int64_t>(row_tiles * nb, (int64_t)sms * 8);
-    CK(launch_k(true, b8::k_block8_write_cols<T>, dim3(grid), dim3(256), 0, st, X, (int)n, d, ldx, vec_ok, slots, first,
-                claims, codes, scales, m->rows, pitch, b8::FastDiv((uint32_t)row_tiles), m->status));
+    CK(launch_k(true, b8::k_block8_write_cols<T>, dim3(grid), dim3(256), 0, st, X, (int)n, d, ldx,
+                b8::vector_width<T>(X, ldx), slots, first, claims, codes, scales, m->rows, pitch, b8::FastDiv((uint32_t)row_tiles), m->status));
     return EM_OK;
 }
 
@@ -164,9 +164,10 @@ template <class T>
 int b8_read_as(const em_block8_t* m, int64_t first, const int64_t* slots, int64_t n, void* out, int64_t ldo,
                int64_t columns, int sms, cudaStream_t st) {
     const int64_t nb = b8_blocks(m->d);
-    CK(launch_k(true, b8::k_block8_read<T>, dim3(b8_pair_grid(n, nb, sms)), dim3(256), 0, st,
+    CK(launch_k(true, slots ? b8::k_block8_read<T, true> : b8::k_block8_read<T, false>,
+                dim3(b8_pair_grid(n, nb, sms)), dim3(256), 0, st,
                 static_cast<const uint8_t*>(m->codes), static_cast<const uint8_t*>(m->scales), m->rows,
-                (int)b8_pitch(m->d), (int)m->d, slots, first, (int)n, static_cast<T*>(out), ldo, (int)columns,
+                (int)b8_pitch(m->d), (int)m->d, slots, (int)first, (int)n, static_cast<T*>(out), ldo, (int)columns,
                 b8::vector_width<T>(out, ldo), b8::FastDiv((uint32_t)nb), m->status));
     return EM_OK;
 }
@@ -245,7 +246,7 @@ int b8_launch_matmul(const em_block8_t* a, int64_t na, const em_block8_t* b, int
     const int64_t t1 = ((na + 127) / 128) * ((nb + 127) / 128);
     const int64_t t2 = ((na + 255) / 256) * ((nb + b8::kPairN - 1) / b8::kPairN);
     const int64_t pairs = std::max(sms / 2, 1);
-    const bool pair = !swap && (t2 + pairs - 1) / pairs * 384 <= (t1 + sms - 1) / sms * 400;
+    const bool pair = !swap && t1 > sms && (t2 + pairs - 1) / pairs * 384 <= (t1 + sms - 1) / sms * 400;
     const bool narrow = swap && nb <= 32;
     const int box_b = pair ? b8::kPairN / 2 : narrow ? 32 : 128;
     CUtensorMap tmA, tmB, tmSA, tmSB;

@@ -215,41 +215,47 @@ constexpr int kPairsPerWarp = 2 * kSteps;
 
 // Writes rows (values of a row contiguous, rows `ldx` apart): a block's values are
 // read once, stay in registers, and leave as codes.
-template <class T>
+template <class T, bool SLOTS>
 __global__ void __launch_bounds__(256)
     k_block8_write(const T* __restrict__ X, int n, int d, int64_t ldx, int width, const int64_t* __restrict__ slots,
-                   int64_t first, const int* __restrict__ claims, uint8_t* __restrict__ codes,
+                   int first, const int* __restrict__ claims, uint8_t* __restrict__ codes,
                    uint8_t* __restrict__ scales, int64_t rows, int pitch, FastDiv nb, int* status) {
     pdl_wait();
     pdl_release();
     const int lane = threadIdx.x & 31, half = lane >> 4, col8 = (lane & 15) * 8;
     const uint32_t total = (uint32_t)n * nb.div;
     const uint32_t stride = gridDim.x * (blockDim.x >> 5) * kPairsPerWarp;
-    const int groups = (int)(nb.div + 3) / 4;
+    const int nbi = (int)nb.div, groups = (nbi + 3) / 4;
     for (uint32_t f0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kPairsPerWarp; f0 < total; f0 += stride) {
         float v[kSteps][8];
-        uint32_t row[kSteps];
-        int64_t dest[kSteps];
-        int b[kSteps];
+        int row[kSteps], b[kSteps], to[kSteps];
+        row[0] = (int)nb.quotient(f0 + half);
+        b[0] = (int)(f0 + half) - row[0] * nbi;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            const uint32_t f = f0 + 2 * s + half;
-            row[s] = nb.quotient(f);
-            b[s] = (int)(f - row[s] * nb.div);
-            dest[s] = f < total ? slot_of(slots, first, row[s], rows, status) : -1;
+            if (s > 0) {  // two pairs on: one row at most, or two where a row is one block
+                b[s] = b[s - 1] + 2;
+                row[s] = row[s - 1];
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (b[s] >= nbi) {
+                        b[s] -= nbi;
+                        ++row[s];
+                    }
+            }
+            to[s] = -1;
+            if (row[s] < n) to[s] = SLOTS ? (int)slot_of(slots, 0, row[s], rows, status) : first + row[s];
         }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            const uint32_t f = f0 + 2 * s + half;
             const int col = b[s] * kBlock + col8;
-            load8(X + (int64_t)row[s] * ldx + col, f < total ? d - col : 0, width, v[s]);
+            load8(X + (int64_t)row[s] * ldx + col, row[s] < n ? d - col : 0, width, v[s]);
         }
-        int mine = 0;       // lane 16 half + s keeps the exponent byte of step s
+        int mine = 0;  // lane 16 half + s keeps the exponent byte of step s
         int64_t place = -1;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            int64_t to = dest[s];
-            if (slots && !last_of_slot(slots, claims, row[s], n, to, lane & 15, 16)) to = -1;
+            if (SLOTS && !last_of_slot(slots, claims, row[s], n, to[s], lane & 15, 16)) to[s] = -1;
             float a = fabsf(v[s][0]);
 #pragma unroll
             for (int t = 1; t < 8; ++t) a = fmaxf(a, fabsf(v[s][t]));  // (fmaxf passes over NaN)
@@ -268,13 +274,13 @@ __global__ void __launch_bounds__(256)
             const int e = block_exponent(half ? hi : lo);
             const float inverse = __uint_as_float((uint32_t)(127 - e) << 23);
             const int col = b[s] * kBlock + col8;
-            if (to >= 0 && col < pitch) {
+            if (to[s] >= 0 && col < pitch) {
                 const uint2 c = make_uint2(encode4(v[s], inverse), encode4(v[s] + 4, inverse));
-                *reinterpret_cast<uint2*>(codes + to * pitch + col) = c;
+                *reinterpret_cast<uint2*>(codes + (int64_t)to[s] * pitch + col) = c;
             }
             if ((lane & 15) == s) {
                 mine = e + 127;
-                place = to < 0 ? -1 : scale_at(to, b[s], groups);
+                place = to[s] < 0 ? -1 : scale_at(to[s], b[s], groups);
             }
         }
         if (place >= 0) scales[place] = (uint8_t)mine;
@@ -282,99 +288,164 @@ __global__ void __launch_bounds__(256)
 }
 
 // Writes rows given as columns: value j of row i is X[j * ldx + i], so consecutive
-// rows are contiguous in memory. A block of 256 threads takes 64 rows x one block of
-// 128 values: warp w loads values 16 w .. 16 w + 15, two rows per lane, and keeps
-// them in registers; the rows' maxima meet in shared memory; the codes are turned in
-// shared memory and leave as 128 bytes per row.
-constexpr int kColRows = 64;
+// rows are contiguous in memory. A block of 256 threads takes a tile of one block of
+// 128 values x kRows rows, 128 bytes of X for each value: a thread loads 16 bytes (V
+// rows) of 4 consecutive values, so that its codes of a row are one word. The rows'
+// maxima (of 16-bit types two to a word) meet by shuffles and in shared memory; the
+// words are turned in shared memory (16-byte pieces of a row XORed with the row's group
+// of V, which keeps both sides off each other's banks) and leave as 128 bytes per row.
+// 64 registers, so that four blocks share an SM: with the values kept as floats it
+// took 100, and 46 us instead of 30 for 1,000 rows of 30,001 fp16 values.
+template <class T>
+struct ColTile {
+    static constexpr int V = 16 / (int)sizeof(T);
+    static constexpr int kRows = 8 * V;
+    static constexpr int kPerWord = 4 / (int)sizeof(T);
+    static constexpr uint32_t kAbs = sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+};
+
+// Words of magnitudes: the larger of each part; NaN gives way.
+template <class T> __device__ __forceinline__ uint32_t max_parts(uint32_t a, uint32_t b);
+template <> __device__ __forceinline__ uint32_t max_parts<float>(uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+}
+template <> __device__ __forceinline__ uint32_t max_parts<__nv_bfloat16>(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <> __device__ __forceinline__ uint32_t max_parts<__half>(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Part s of a word as fp32, and an fp32 value put in its place.
+template <class T>
+__device__ __forceinline__ float part_of(uint32_t w, int s) {
+    if (sizeof(T) == 4) return __uint_as_float(w);
+    const uint16_t h = (uint16_t)(w >> (16 * s));
+    T v;
+    memcpy(&v, &h, sizeof(T) < 2 ? sizeof(T) : 2);
+    return to_f32(v);
+}
+template <class T>
+__device__ __forceinline__ uint32_t with_part(uint32_t w, int s, float f) {
+    if (sizeof(T) == 4) return __float_as_uint(f);
+    const T v = from_f32<T>(f);
+    uint16_t h;
+    memcpy(&h, &v, 2);
+    return s ? (w & 0xFFFFu) | ((uint32_t)h << 16) : (w & 0xFFFF0000u) | h;
+}
 
 template <class T>
-__global__ void __launch_bounds__(256)
-    k_block8_write_cols(const T* __restrict__ X, int n, int d, int64_t ldx, int vec_ok,
+__global__ void __launch_bounds__(256, 4)
+    k_block8_write_cols(const T* __restrict__ X, int n, int d, int64_t ldx, int width,
                         const int64_t* __restrict__ slots, int64_t first, const int* __restrict__ claims,
                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t rows, int pitch,
                         FastDiv row_tiles, int* status) {
-    constexpr int kPitch = kBlock + 16;
-    __shared__ float amax[8][kColRows];
-    __shared__ __align__(16) uint8_t turned[kColRows * kPitch];
-    __shared__ int64_t dest[kColRows];
+    using C = ColTile<T>;
+    constexpr int V = C::V, kRows = C::kRows, PW = C::kPerWord;
+    __shared__ __align__(16) uint32_t amax[8][kRows / PW];
+    __shared__ __align__(16) uint8_t turned[kRows * kBlock];
+    __shared__ int dest[kRows];
     pdl_wait();
     pdl_release();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int k = threadIdx.x & 7, jq = threadIdx.x >> 3;  // which V rows, which 4 values
     const int nb = (d + kBlock - 1) / kBlock, groups = (nb + 3) / 4;
     const uint32_t tiles = row_tiles.div * (uint32_t)nb;
     for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int b = (int)row_tiles.quotient(t), base = (int)(t - (uint32_t)b * row_tiles.div) * kColRows;
-        const int i0 = base + 2 * lane, j0 = b * kBlock + 16 * w;
-        float v[2][16];
+        const int b = (int)row_tiles.quotient(t), base = (int)(t - (uint32_t)b * row_tiles.div) * kRows;
+        const int i0 = base + V * k, j0 = b * kBlock + 4 * jq;
         const T* src = X + (int64_t)j0 * ldx + i0;
-        if (vec_ok && i0 + 2 <= n && j0 + 16 <= d) {  // (no branch between the loads: all 16 are in flight together)
-            Vec<T, 2> x[16];
+        uint32_t x[4][4];
+        if (width == V && i0 + V <= n && j0 + 4 <= d) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = *reinterpret_cast<const Vec<T, 2>*>(src + k * ldx);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                v[0][k] = to_f32(x[k].v[0]);
-                v[1][k] = to_f32(x[k].v[1]);
+            for (int q = 0; q < 4; ++q) {
+                const uint4 u = *reinterpret_cast<const uint4*>(src + q * ldx);
+                x[q][0] = u.x; x[q][1] = u.y; x[q][2] = u.z; x[q][3] = u.w;
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                v[0][k] = j0 + k < d && i0 < n ? to_f32(src[k * ldx]) : 0.0f;
-                v[1][k] = j0 + k < d && i0 + 1 < n ? to_f32(src[k * ldx + 1]) : 0.0f;
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int r = 0; r < V; ++r) {
+                    const float f = j0 + q < d && i0 + r < n ? to_f32(src[q * ldx + r]) : 0.0f;
+                    x[q][r / PW] = with_part<T>(r % PW ? x[q][r / PW] : 0u, r % PW, f);
+                }
+        }
+        // where the tile's rows go
+        if (slots)
+            for (int r = w; r < kRows; r += 8) {
+                const int i = base + r;
+                int64_t to = i < n ? slot_of(slots, first, i, rows, status) : -1;
+                if (!last_of_slot(slots, claims, i, n, to, lane, 32)) to = -1;
+                if (lane == 0) dest[r] = (int)to;
             }
+        uint32_t a[4], top = 0u;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            a[h] = 0u;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) a[h] = max_parts<T>(a[h], x[q][h] & C::kAbs);
+            top = max_parts<T>(top, a[h]);
         }
-        // where the tile's rows go (8 rows per warp)
-        for (int r = w * (kColRows / 8); r < (w + 1) * (kColRows / 8); ++r) {
-            const int i = base + r;
-            int64_t to = i < n ? slot_of(slots, first, i, rows, status) : -1;
-            if (slots && !last_of_slot(slots, claims, i, n, to, lane, 32)) to = -1;
-            if (lane == 0) dest[r] = to;
-        }
-        float a[2] = {0.0f, 0.0f};
+        if (isinf(part_of<T>(top, 0)) || isinf(part_of<T>(top, PW - 1))) {
+            // an infinity: held as NaN, the block scaled by the others
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+            for (int h = 0; h < 4; ++h) {
+                a[h] = 0u;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) a[r] = fmaxf(a[r], fabsf(v[r][k]));
-            if (__float_as_uint(a[r]) >= 0x7F800000u) {  // (as in k_block8_write)
-                a[r] = 0.0f;
+                for (int q = 0; q < 4; ++q) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    v[r][k] = finite_or_nan(v[r][k]);
-                    a[r] = fmaxf(a[r], fabsf(v[r][k]));
+                    for (int s = 0; s < PW; ++s)
+                        x[q][h] = with_part<T>(x[q][h], s, finite_or_nan(part_of<T>(x[q][h], s)));
+                    a[h] = max_parts<T>(a[h], x[q][h] & C::kAbs);
                 }
             }
         }
-        *reinterpret_cast<float2*>(&amax[w][2 * lane]) = make_float2(a[0], a[1]);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            a[h] = max_parts<T>(a[h], __shfl_xor_sync(0xFFFFFFFFu, a[h], 8));
+            a[h] = max_parts<T>(a[h], __shfl_xor_sync(0xFFFFFFFFu, a[h], 16));
+        }
+        if (lane < 8) *reinterpret_cast<uint4*>(&amax[w][4 * k]) = make_uint4(a[0], a[1], a[2], a[3]);
         __syncthreads();
-        float m[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) a[h] = 0u;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            const float2 x = *reinterpret_cast<const float2*>(&amax[q][2 * lane]);
-            m[0] = fmaxf(m[0], x.x);
-            m[1] = fmaxf(m[1], x.y);
+            const uint4 f = *reinterpret_cast<const uint4*>(&amax[q][4 * k]);
+            a[0] = max_parts<T>(a[0], f.x);
+            a[1] = max_parts<T>(a[1], f.y);
+            a[2] = max_parts<T>(a[2], f.z);
+            a[3] = max_parts<T>(a[3], f.w);
         }
+        int mine = 0;  // the exponent of row jq of the thread's V
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int e = block_exponent(__float_as_uint(m[r]));
+        for (int r = 0; r < V; ++r) {
+            const int e = block_exponent(__float_as_uint(part_of<T>(a[r / PW], r % PW)));
             const float inverse = __uint_as_float((uint32_t)(127 - e) << 23);
-            *reinterpret_cast<uint4*>(turned + (2 * lane + r) * kPitch + 16 * w) =
-                make_uint4(encode4(v[r], inverse), encode4(v[r] + 4, inverse), encode4(v[r] + 8, inverse),
-                           encode4(v[r] + 12, inverse));
-            if (w == r) {
-                const int64_t to = dest[2 * lane + r];
-                if (to >= 0) scales[scale_at(to, b, groups)] = (uint8_t)(e + 127);
-            }
+            const float v[4] = {part_of<T>(x[0][r / PW], r % PW), part_of<T>(x[1][r / PW], r % PW),
+                                part_of<T>(x[2][r / PW], r % PW), part_of<T>(x[3][r / PW], r % PW)};
+            *reinterpret_cast<uint32_t*>(turned + (V * k + r) * kBlock + 4 * (jq ^ (4 * k))) = encode4(v, inverse);
+            mine = jq == r ? e : mine;
+        }
+        if (jq < V) {
+            const int i = i0 + jq;
+            const int to = slots ? dest[V * k + jq] : i < n ? (int)first + i : -1;
+            if (to >= 0) scales[scale_at(to, b, groups)] = (uint8_t)(mine + 127);
         }
         __syncthreads();
         // 8 threads per row, 16 codes each
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int r = (threadIdx.x >> 3) + 32 * q, c = (threadIdx.x & 7) * 16;
-            const int64_t to = dest[r];
-            if (to >= 0 && b * kBlock + c < pitch)
-                *reinterpret_cast<uint4*>(codes + to * pitch + b * kBlock + c) =
-                    *reinterpret_cast<const uint4*>(turned + r * kPitch + c);
+        for (int q = 0; q < kRows / 32; ++q) {
+            const int r = (threadIdx.x >> 3) + 32 * q, c = threadIdx.x & 7;
+            const int to = slots ? dest[r] : base + r < n ? (int)first + base + r : -1;
+            if (to >= 0 && b * kBlock + 16 * c < pitch)
+                *reinterpret_cast<uint4*>(codes + (int64_t)to * pitch + b * kBlock + 16 * c) =
+                    *reinterpret_cast<const uint4*>(turned + r * kBlock + 16 * (c ^ (r / V)));
         }
         __syncthreads();
     }
@@ -383,50 +454,74 @@ __global__ void __launch_bounds__(256)
 // Reads rows back, pairs as in k_block8_write. Exact in fp32 and bf16; fp16 rounds to
 // nearest even (and overflows to infinity). Padding rows (slot -1) and rows outside
 // the matrix read as zeros. `columns` values are written for each row, zeros past d.
-template <class T>
-__global__ void __launch_bounds__(256)
+// What bounds it is issue: 8 values are 27 instructions to load, decode, scale and
+// store, and finding them must not cost as much again (32-bit row numbers, the next
+// pair by steps, no branch between the loads).
+template <class T, bool SLOTS>
+__global__ void __launch_bounds__(256, 5)
     k_block8_read(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int pitch,
-                  int d, const int64_t* __restrict__ slots, int64_t first, int n, T* __restrict__ out, int64_t ldo,
+                  int d, const int64_t* __restrict__ slots, int first, int n, T* __restrict__ out, int64_t ldo,
                   int columns, int width, FastDiv nb, int* status) {
     pdl_wait();
     pdl_release();
     const int lane = threadIdx.x & 31, half = lane >> 4, col8 = (lane & 15) * 8;
     const uint32_t total = (uint32_t)n * nb.div;
     const uint32_t stride = gridDim.x * (blockDim.x >> 5) * kPairsPerWarp;
-    const int groups = (int)(nb.div + 3) / 4;
+    const int nbi = (int)nb.div, groups = (nbi + 3) / 4;
     for (uint32_t f0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kPairsPerWarp; f0 < total; f0 += stride) {
         uint2 c[kSteps];
         uint8_t byte[kSteps];
-        uint32_t row[kSteps];
-        int64_t from[kSteps];
-        int col[kSteps];
+        int row[kSteps], b[kSteps], from[kSteps];
+        row[0] = (int)nb.quotient(f0 + half);
+        b[0] = (int)(f0 + half) - row[0] * nbi;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            const uint32_t f = f0 + 2 * s + half;
-            row[s] = nb.quotient(f);
-            col[s] = (int)(f - row[s] * nb.div) * kBlock + col8;
-            from[s] = f < total ? slot_of(slots, first, row[s], rows, status) : -1;
+            if (s > 0) {  // two pairs on: one row at most, or two where a row is one block
+                b[s] = b[s - 1] + 2;
+                row[s] = row[s - 1];
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (b[s] >= nbi) {
+                        b[s] -= nbi;
+                        ++row[s];
+                    }
+            }
+            from[s] = -1;
+            if (row[s] < n) {
+                if (SLOTS) {
+                    const int64_t at = slots[row[s]];
+                    if (at >= 0 && at < rows)
+                        from[s] = (int)at;
+                    else if (at != -1)
+                        raise_error(status, EM_E_BOUNDS);
+                } else {
+                    from[s] = first + row[s];
+                }
+            }
         }
         // (a row that is left out loads row 0 and drops it, so that no branch parts the loads)
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            const int64_t r = max(from[s], (int64_t)0);
-            c[s] = *reinterpret_cast<const uint2*>(codes + r * pitch + min(col[s], pitch - 8));
-            byte[s] = scales[scale_at(r, col[s] / kBlock, groups)];
+            const int r = max(from[s], 0);
+            c[s] = *reinterpret_cast<const uint2*>(codes + (int64_t)r * pitch + min(b[s] * kBlock + col8, pitch - 8));
+            byte[s] = scales[scale_at(r, b[s], groups)];
         }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
+            if (row[s] >= n) break;
+            const int col = b[s] * kBlock + col8;
+            if (from[s] < 0) c[s] = make_uint2(0u, 0u);
+            const float scale = scale_of(byte[s]);
             float v[8];
             decode4(c[s].x, v);
             decode4(c[s].y, v + 4);
 #pragma unroll
-            for (int t = 0; t < 8; ++t) v[t] = from[s] >= 0 ? v[t] * scale_of(byte[s]) : 0.0f;
-            if (col[s] + 8 > d) {
+            for (int t = 0; t < 8; ++t) v[t] *= scale;
+            if (col + 8 > d) {
 #pragma unroll
-                for (int t = 0; t < 8; ++t) v[t] = col[s] + t < d ? v[t] : 0.0f;
+                for (int t = 0; t < 8; ++t) v[t] = col + t < d ? v[t] : 0.0f;
             }
-            const int left = f0 + 2 * s + half < total ? columns - col[s] : 0;
-            store8(out + (int64_t)row[s] * ldo + col[s], left, width, v);
+            store8(out + (int64_t)row[s] * ldo + col, columns - col, width, v);
         }
     }
 }
