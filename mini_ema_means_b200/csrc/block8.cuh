@@ -134,8 +134,12 @@ int b8_device(int dev, DeviceFacts* out) {
     return EM_OK;
 }
 
+// Blocks per SM at most: many more than fit, so that the last ones even out (65,536 x
+// 768 fp32 read back: 46 us, with the 8 per SM that fit 53).
+constexpr int kB8PerSm = 64;
+
 int b8_pair_grid(int64_t n, int64_t nb, int sms) {
-    return grid_for((n * nb + b8::kPairsPerWarp - 1) / b8::kPairsPerWarp * 32, 256, sms, 8);
+    return grid_for((n * nb + b8::kPairsPerWarp - 1) / b8::kPairsPerWarp * 32, 256, sms, kB8PerSm);
 }
 
 template <class T>
@@ -147,10 +151,12 @@ int b8_write(bool cols, const void* X_, int64_t n, int64_t ldx, const int64_t* s
     const int64_t nb = b8_blocks(m->d);
     const int d = (int)m->d, pitch = (int)b8_pitch(m->d);
     if (!cols) {
-        CK(launch_k(true, slots ? b8::k_block8_write<T, true> : b8::k_block8_write<T, false>,
-                    dim3(b8_pair_grid(n, nb, sms)), dim3(256), 0, st, X, (int)n, d, ldx, b8::vector_width<T>(X, ldx), slots,
-                    (int)first, claims, codes, scales, m->rows, pitch,
-                    b8::FastDiv((uint32_t)nb), m->status));
+        const int width = b8::vector_width<T>(X, ldx);
+        const bool fast = width * sizeof(T) == 16 && d % 8 == 0;
+        auto* kernel = slots ? (fast ? b8::k_block8_write<T, true, true> : b8::k_block8_write<T, true, false>)
+                             : (fast ? b8::k_block8_write<T, false, true> : b8::k_block8_write<T, false, false>);
+        CK(launch_k(true, kernel, dim3(b8_pair_grid(n, nb, sms)), dim3(256), 0, st, X, (int)n, d, ldx, width, slots,
+                    (int)first, claims, codes, scales, m->rows, pitch, b8::FastDiv((uint32_t)nb), m->status));
         return EM_OK;
     }
     const int64_t row_tiles = (n + b8::ColTile<T>::kRows - 1) / b8::ColTile<T>::kRows;
@@ -164,11 +170,14 @@ template <class T>
 int b8_read_as(const em_block8_t* m, int64_t first, const int64_t* slots, int64_t n, void* out, int64_t ldo,
                int64_t columns, int sms, cudaStream_t st) {
     const int64_t nb = b8_blocks(m->d);
-    CK(launch_k(true, slots ? b8::k_block8_read<T, true> : b8::k_block8_read<T, false>,
-                dim3(b8_pair_grid(n, nb, sms)), dim3(256), 0, st,
+    const int width = b8::vector_width<T>(out, ldo);
+    const bool fast = width * sizeof(T) == 16 && m->d % 8 == 0 && columns == m->d;
+    auto* kernel = slots ? (fast ? b8::k_block8_read<T, true, true> : b8::k_block8_read<T, true, false>)
+                         : (fast ? b8::k_block8_read<T, false, true> : b8::k_block8_read<T, false, false>);
+    CK(launch_k(true, kernel, dim3(b8_pair_grid(n, nb, sms)), dim3(256), 0, st,
                 static_cast<const uint8_t*>(m->codes), static_cast<const uint8_t*>(m->scales), m->rows,
-                (int)b8_pitch(m->d), (int)m->d, slots, (int)first, (int)n, static_cast<T*>(out), ldo, (int)columns,
-                b8::vector_width<T>(out, ldo), b8::FastDiv((uint32_t)nb), m->status));
+                (int)b8_pitch(m->d), (int)m->d, slots, (int)first, (int)n, static_cast<T*>(out), ldo, (int)columns, width,
+                b8::FastDiv((uint32_t)nb), m->status));
     return EM_OK;
 }
 

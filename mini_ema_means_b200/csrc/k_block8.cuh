@@ -207,103 +207,6 @@ __device__ __forceinline__ bool last_of_slot(const int64_t* __restrict__ slots, 
     return ((all >> shift) & (lanes == 32 ? 0xFFFFFFFFu : 0xFFFFu)) == 0u;
 }
 
-// The work of the row kernels: (row, block) pairs in row order, 16 lanes per pair with
-// 8 consecutive values each, two pairs per warp and step, kSteps steps in flight.
-// Short rows fill a warp as well as long ones (a row of 96 values is one pair).
-constexpr int kSteps = 4;
-constexpr int kPairsPerWarp = 2 * kSteps;
-
-// Writes rows (values of a row contiguous, rows `ldx` apart): a block's values are
-// read once, stay in registers, and leave as codes.
-template <class T, bool SLOTS>
-__global__ void __launch_bounds__(256)
-    k_block8_write(const T* __restrict__ X, int n, int d, int64_t ldx, int width, const int64_t* __restrict__ slots,
-                   int first, const int* __restrict__ claims, uint8_t* __restrict__ codes,
-                   uint8_t* __restrict__ scales, int64_t rows, int pitch, FastDiv nb, int* status) {
-    pdl_wait();
-    pdl_release();
-    const int lane = threadIdx.x & 31, half = lane >> 4, col8 = (lane & 15) * 8;
-    const uint32_t total = (uint32_t)n * nb.div;
-    const uint32_t stride = gridDim.x * (blockDim.x >> 5) * kPairsPerWarp;
-    const int nbi = (int)nb.div, groups = (nbi + 3) / 4;
-    for (uint32_t f0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kPairsPerWarp; f0 < total; f0 += stride) {
-        float v[kSteps][8];
-        int row[kSteps], b[kSteps], to[kSteps];
-        row[0] = (int)nb.quotient(f0 + half);
-        b[0] = (int)(f0 + half) - row[0] * nbi;
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            if (s > 0) {  // two pairs on: one row at most, or two where a row is one block
-                b[s] = b[s - 1] + 2;
-                row[s] = row[s - 1];
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    if (b[s] >= nbi) {
-                        b[s] -= nbi;
-                        ++row[s];
-                    }
-            }
-            to[s] = -1;
-            if (row[s] < n) to[s] = SLOTS ? (int)slot_of(slots, 0, row[s], rows, status) : first + row[s];
-        }
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int col = b[s] * kBlock + col8;
-            load8(X + (int64_t)row[s] * ldx + col, row[s] < n ? d - col : 0, width, v[s]);
-        }
-        int mine = 0;  // lane 16 half + s keeps the exponent byte of step s
-        int64_t place = -1;
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            if (SLOTS && !last_of_slot(slots, claims, row[s], n, to[s], lane & 15, 16)) to[s] = -1;
-            float a = fabsf(v[s][0]);
-#pragma unroll
-            for (int t = 1; t < 8; ++t) a = fmaxf(a, fabsf(v[s][t]));  // (fmaxf passes over NaN)
-            uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, half ? 0u : __float_as_uint(a));
-            uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, half ? __float_as_uint(a) : 0u);
-            if (max(lo, hi) >= 0x7F800000u) {  // an infinity (or NaN alone): hold it as NaN, scale by the others
-                a = 0.0f;
-#pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    v[s][t] = finite_or_nan(v[s][t]);
-                    a = fmaxf(a, fabsf(v[s][t]));
-                }
-                lo = __reduce_max_sync(0xFFFFFFFFu, half ? 0u : __float_as_uint(a));
-                hi = __reduce_max_sync(0xFFFFFFFFu, half ? __float_as_uint(a) : 0u);
-            }
-            const int e = block_exponent(half ? hi : lo);
-            const float inverse = __uint_as_float((uint32_t)(127 - e) << 23);
-            const int col = b[s] * kBlock + col8;
-            if (to[s] >= 0 && col < pitch) {
-                const uint2 c = make_uint2(encode4(v[s], inverse), encode4(v[s] + 4, inverse));
-                *reinterpret_cast<uint2*>(codes + (int64_t)to[s] * pitch + col) = c;
-            }
-            if ((lane & 15) == s) {
-                mine = e + 127;
-                place = to[s] < 0 ? -1 : scale_at(to[s], b[s], groups);
-            }
-        }
-        if (place >= 0) scales[place] = (uint8_t)mine;
-    }
-}
-
-// Writes rows given as columns: value j of row i is X[j * ldx + i], so consecutive
-// rows are contiguous in memory. A block of 256 threads takes a tile of one block of
-// 128 values x kRows rows, 128 bytes of X for each value: a thread loads 16 bytes (V
-// rows) of 4 consecutive values, so that its codes of a row are one word. The rows'
-// maxima (of 16-bit types two to a word) meet by shuffles and in shared memory; the
-// words are turned in shared memory (16-byte pieces of a row XORed with the row's group
-// of V, which keeps both sides off each other's banks) and leave as 128 bytes per row.
-// 64 registers, so that four blocks share an SM: with the values kept as floats it
-// took 100, and 46 us instead of 30 for 1,000 rows of 30,001 fp16 values.
-template <class T>
-struct ColTile {
-    static constexpr int V = 16 / (int)sizeof(T);
-    static constexpr int kRows = 8 * V;
-    static constexpr int kPerWord = 4 / (int)sizeof(T);
-    static constexpr uint32_t kAbs = sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
-};
-
 // Words of magnitudes: the larger of each part; NaN gives way.
 template <class T> __device__ __forceinline__ uint32_t max_parts(uint32_t a, uint32_t b);
 template <> __device__ __forceinline__ uint32_t max_parts<float>(uint32_t a, uint32_t b) {
@@ -337,6 +240,155 @@ __device__ __forceinline__ uint32_t with_part(uint32_t w, int s, float f) {
     memcpy(&h, &v, 2);
     return s ? (w & 0xFFFFu) | ((uint32_t)h << 16) : (w & 0xFFFF0000u) | h;
 }
+
+// The work of the row kernels: (row, block) pairs in row order, 16 lanes per pair with
+// 8 consecutive values each, two pairs per warp and step, kSteps steps in flight.
+// Short rows fill a warp as well as long ones (a row of 96 values is one pair).
+constexpr int kSteps = 4;
+constexpr int kPairsPerWarp = 2 * kSteps;
+
+// The (row, block) pairs of a lane: first the pair `f`, then every second one.
+struct Pairs {
+    int row[kSteps], b[kSteps];
+    __device__ __forceinline__ Pairs(uint32_t f, const FastDiv& nb) {
+        const int nbi = (int)nb.div;
+        row[0] = (int)nb.quotient(f);
+        b[0] = (int)f - row[0] * nbi;
+#pragma unroll
+        for (int s = 1; s < kSteps; ++s) {  // one row on at most, or two where a row is one block
+            b[s] = b[s - 1] + 2;
+            row[s] = row[s - 1];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (b[s] >= nbi) {
+                    b[s] -= nbi;
+                    ++row[s];
+                }
+        }
+    }
+};
+
+// 8 values of type T as words; FAST: one or two 16-byte loads.
+template <class T>
+struct Eight {
+    static constexpr int kWords = 2 * (int)sizeof(T), PW = 4 / (int)sizeof(T);
+    static constexpr uint32_t kAbs = sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load_fast(const T* p) {
+#pragma unroll
+        for (int q = 0; q < kWords; q += 4) {
+            const uint4 u = reinterpret_cast<const uint4*>(p)[q / 4];
+            w[q] = u.x; w[q + 1] = u.y; w[q + 2] = u.z; w[q + 3] = u.w;
+        }
+    }
+    __device__ __forceinline__ void load(const T* p, int left, int width) {
+        float v[8];
+        load8(p, left, width, v);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) w[t / PW] = with_part<T>(t % PW ? w[t / PW] : 0u, t % PW, v[t]);
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int q = 0; q < kWords; ++q) w[q] = 0u;
+    }
+    // the bits of the largest magnitude as fp32 (infinity where there is one; NaN gives way)
+    __device__ __forceinline__ uint32_t largest() const {
+        uint32_t a = w[0] & kAbs;
+#pragma unroll
+        for (int q = 1; q < kWords; ++q) a = max_parts<T>(a, w[q] & kAbs);
+        if (PW == 1) return a;
+        return __float_as_uint(fmaxf(part_of<T>(a, 0), part_of<T>(a, 1)));
+    }
+    __device__ __forceinline__ void drop_infinities() {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            w[t / PW] = with_part<T>(w[t / PW], t % PW, finite_or_nan(part_of<T>(w[t / PW], t % PW)));
+    }
+    __device__ __forceinline__ uint2 encode(float inverse) const {
+        float v[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) v[t] = part_of<T>(w[t / PW], t % PW);
+        return make_uint2(encode4(v, inverse), encode4(v + 4, inverse));
+    }
+};
+
+// Writes rows (values of a row contiguous, rows `ldx` apart): a block's values are
+// read once, stay in registers as they came, and leave as codes. FAST: rows are
+// 16-byte aligned and d is a multiple of 8; lanes past the data then load a place
+// inside it and drop it, so that no branch parts the loads.
+template <class T, bool SLOTS, bool FAST>
+__global__ void __launch_bounds__(256)
+    k_block8_write(const T* __restrict__ X, int n, int d, int64_t ldx, int width, const int64_t* __restrict__ slots,
+                   int first, const int* __restrict__ claims, uint8_t* __restrict__ codes,
+                   uint8_t* __restrict__ scales, int64_t rows, int pitch, FastDiv nb, int* status) {
+    pdl_wait();
+    pdl_release();
+    const int lane = threadIdx.x & 31, half = lane >> 4, col8 = (lane & 15) * 8;
+    const uint32_t total = (uint32_t)n * nb.div;
+    const uint32_t stride = gridDim.x * (blockDim.x >> 5) * kPairsPerWarp;
+    const int groups = (int)(nb.div + 3) / 4;
+    for (uint32_t f0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kPairsPerWarp; f0 < total; f0 += stride) {
+        const Pairs at(f0 + half, nb);
+        Eight<T> v[kSteps];
+        int to[kSteps];
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int col = at.b[s] * kBlock + col8;
+            if (FAST)
+                v[s].load_fast(X + (int64_t)min(at.row[s], n - 1) * ldx + min(col, d - 8));
+            else
+                v[s].load(X + (int64_t)at.row[s] * ldx + col, at.row[s] < n ? d - col : 0, width);
+        }
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            to[s] = -1;
+            if (at.row[s] < n) to[s] = SLOTS ? (int)slot_of(slots, 0, at.row[s], rows, status) : first + at.row[s];
+        }
+        int mine = 0, my_to = -1, my_b = 0;  // lane 16 half + s keeps the exponent of step s
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int col = at.b[s] * kBlock + col8;
+            if (SLOTS && !last_of_slot(slots, claims, at.row[s], n, to[s], lane & 15, 16)) to[s] = -1;
+            if (FAST && col >= d) v[s].clear();
+            uint32_t a = v[s].largest();
+            uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, half ? 0u : a), hi = __reduce_max_sync(0xFFFFFFFFu, half ? a : 0u);
+            if (max(lo, hi) >= 0x7F800000u) {  // an infinity (or NaN alone): held as NaN, the block scaled by the others
+                v[s].drop_infinities();
+                a = v[s].largest();
+                if (a >= 0x7F800000u) a = 0u;  // NaN alone
+                lo = __reduce_max_sync(0xFFFFFFFFu, half ? 0u : a);
+                hi = __reduce_max_sync(0xFFFFFFFFu, half ? a : 0u);
+            }
+            const int e = block_exponent(half ? hi : lo);
+            const float inverse = __uint_as_float((uint32_t)(127 - e) << 23);
+            if (to[s] >= 0 && col < pitch)
+                *reinterpret_cast<uint2*>(codes + (int64_t)to[s] * pitch + col) = v[s].encode(inverse);
+            if ((lane & 15) == s) {
+                mine = e + 127;
+                my_to = to[s];
+                my_b = at.b[s];
+            }
+        }
+        if (my_to >= 0) scales[scale_at(my_to, my_b, groups)] = (uint8_t)mine;
+    }
+}
+
+// Writes rows given as columns: value j of row i is X[j * ldx + i], so consecutive
+// rows are contiguous in memory. A block of 256 threads takes a tile of one block of
+// 128 values x kRows rows, 128 bytes of X for each value: a thread loads 16 bytes (V
+// rows) of 4 consecutive values, so that its codes of a row are one word. The rows'
+// maxima (of 16-bit types two to a word) meet by shuffles and in shared memory; the
+// words are turned in shared memory (16-byte pieces of a row XORed with the row's group
+// of V, which keeps both sides off each other's banks) and leave as 128 bytes per row.
+// 64 registers, so that four blocks share an SM: with the values kept as floats it
+// took 100, and 46 us instead of 30 for 1,000 rows of 30,001 fp16 values.
+template <class T>
+struct ColTile {
+    static constexpr int V = 16 / (int)sizeof(T);
+    static constexpr int kRows = 8 * V;
+    static constexpr int kPerWord = 4 / (int)sizeof(T);
+    static constexpr uint32_t kAbs = sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+};
 
 template <class T>
 __global__ void __launch_bounds__(256, 4)
@@ -457,7 +509,7 @@ __global__ void __launch_bounds__(256, 4)
 // What bounds it is issue: 8 values are 27 instructions to load, decode, scale and
 // store, and finding them must not cost as much again (32-bit row numbers, the next
 // pair by steps, no branch between the loads).
-template <class T, bool SLOTS>
+template <class T, bool SLOTS, bool FAST>
 __global__ void __launch_bounds__(256, 5)
     k_block8_read(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int pitch,
                   int d, const int64_t* __restrict__ slots, int first, int n, T* __restrict__ out, int64_t ldo,
@@ -467,49 +519,28 @@ __global__ void __launch_bounds__(256, 5)
     const int lane = threadIdx.x & 31, half = lane >> 4, col8 = (lane & 15) * 8;
     const uint32_t total = (uint32_t)n * nb.div;
     const uint32_t stride = gridDim.x * (blockDim.x >> 5) * kPairsPerWarp;
-    const int nbi = (int)nb.div, groups = (nbi + 3) / 4;
+    const int groups = (int)(nb.div + 3) / 4;
     for (uint32_t f0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kPairsPerWarp; f0 < total; f0 += stride) {
+        const Pairs at(f0 + half, nb);
         uint2 c[kSteps];
         uint8_t byte[kSteps];
-        int row[kSteps], b[kSteps], from[kSteps];
-        row[0] = (int)nb.quotient(f0 + half);
-        b[0] = (int)(f0 + half) - row[0] * nbi;
+        int from[kSteps];
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            if (s > 0) {  // two pairs on: one row at most, or two where a row is one block
-                b[s] = b[s - 1] + 2;
-                row[s] = row[s - 1];
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    if (b[s] >= nbi) {
-                        b[s] -= nbi;
-                        ++row[s];
-                    }
-            }
             from[s] = -1;
-            if (row[s] < n) {
-                if (SLOTS) {
-                    const int64_t at = slots[row[s]];
-                    if (at >= 0 && at < rows)
-                        from[s] = (int)at;
-                    else if (at != -1)
-                        raise_error(status, EM_E_BOUNDS);
-                } else {
-                    from[s] = first + row[s];
-                }
-            }
+            if (at.row[s] < n) from[s] = SLOTS ? (int)slot_of(slots, 0, at.row[s], rows, status) : first + at.row[s];
         }
         // (a row that is left out loads row 0 and drops it, so that no branch parts the loads)
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
             const int r = max(from[s], 0);
-            c[s] = *reinterpret_cast<const uint2*>(codes + (int64_t)r * pitch + min(b[s] * kBlock + col8, pitch - 8));
-            byte[s] = scales[scale_at(r, b[s], groups)];
+            c[s] = *reinterpret_cast<const uint2*>(codes + (int64_t)r * pitch + min(at.b[s] * kBlock + col8, pitch - 8));
+            byte[s] = scales[scale_at(r, at.b[s], groups)];
         }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            if (row[s] >= n) break;
-            const int col = b[s] * kBlock + col8;
+            if (at.row[s] >= n) break;
+            const int col = at.b[s] * kBlock + col8;
             if (from[s] < 0) c[s] = make_uint2(0u, 0u);
             const float scale = scale_of(byte[s]);
             float v[8];
@@ -517,11 +548,16 @@ __global__ void __launch_bounds__(256, 5)
             decode4(c[s].y, v + 4);
 #pragma unroll
             for (int t = 0; t < 8; ++t) v[t] *= scale;
-            if (col + 8 > d) {
+            T* dst = out + (int64_t)at.row[s] * ldo + col;
+            if (FAST) {  // (columns = d, a multiple of 8, and 16-byte aligned rows)
+                if (col < d) store8_as<T, 16 / sizeof(T)>(dst, v);
+            } else {
+                if (col + 8 > d) {
 #pragma unroll
-                for (int t = 0; t < 8; ++t) v[t] = col + t < d ? v[t] : 0.0f;
+                    for (int t = 0; t < 8; ++t) v[t] = col + t < d ? v[t] : 0.0f;
+                }
+                store8(dst, columns - col, width, v);
             }
-            store8(out + (int64_t)row[s] * ldo + col, columns - col, width, v);
         }
     }
 }
