@@ -738,7 +738,7 @@ __device__ __forceinline__ void add_columns(uint32_t taddr, uint32_t (&sum)[32])
 // One warp's 32 rows x Q 16-byte pieces of results (lane = row, 4 Q words w) to rows
 // row0.. and columns col0.. of `out`: turned in the warp's 4 KB of shared memory (a
 // piece's place in its row XORed with the row, so that neither side meets a bank
-// twice), then stored as whole 128-byte row pieces (64 with Q = 4), Q lanes to a row.
+// twice), then stored as whole row pieces, Q lanes to a row.
 template <int OB, int Q>
 __device__ __forceinline__ void store_piece(const uint32_t (&w)[32], uint8_t* buf, int lane, int64_t row0, int64_t col0,
                                             const MmArgs& p) {
@@ -749,30 +749,35 @@ __device__ __forceinline__ void store_piece(const uint32_t (&w)[32], uint8_t* bu
         *reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) =
             make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     __syncwarp();
-    constexpr int kRows = 32 / Q;  // rows per step
-    const int piece = lane % Q, r0 = lane / Q;
-    const int64_t cc = col0 + piece * (16 / OB);  // this lane's first column
-    uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + ((row0 + r0) * p.ldo + cc) * OB;
+    constexpr int kPer = 16 / OB;  // columns of a piece
+    if (p.vec_ok && col0 + Q * kPer <= p.n_rows) {
+        constexpr int kRows = 32 / Q;  // rows per step
+        const int piece = lane % Q, r0 = lane / Q;
+        uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + ((row0 + r0) * p.ldo + col0 + piece * kPer) * OB;
 #pragma unroll
-    for (int i = 0; i < Q; ++i) {
-        const int r = kRows * i + r0;
-        const uint4 x = *reinterpret_cast<const uint4*>(buf + r * 128 + ((piece ^ (r & 7)) << 4));
-        if (row0 + r < p.m_rows) {
-            if (p.vec_ok && cc + 16 / OB <= p.n_rows) {
-                *reinterpret_cast<uint4*>(dst) = x;
-            } else {
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+        for (int i = 0; i < Q; ++i) {
+            const int r = kRows * i + r0;
+            const uint4 x = *reinterpret_cast<const uint4*>(buf + r * 128 + ((piece ^ (r & 7)) << 4));
+            if (row0 + r < p.m_rows) *reinterpret_cast<uint4*>(dst) = x;
+            dst += kRows * p.ldo * OB;
+        }
+        return;
+    }
+    // rows that are not 16-byte aligned, or end inside: 32 neighbouring columns at a time
+    const int rows = (int)min(p.m_rows - row0, (int64_t)32), cols = (int)min(p.n_rows - col0, (int64_t)(Q * kPer));
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r) {
+        uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + ((row0 + r) * p.ldo + col0) * OB;
 #pragma unroll
-                for (int e = 0; e < 16 / OB; ++e)
-                    if (cc + e < p.n_rows) {
-                        if (OB == 4)
-                            reinterpret_cast<uint32_t*>(dst)[e] = xs[e];
-                        else
-                            reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(xs[e >> 1] >> (16 * (e & 1)));
-                    }
+        for (int c = lane; c < Q * kPer; c += 32) {
+            const uint8_t* x = buf + r * 128 + (((c / kPer) ^ (r & 7)) << 4) + c % kPer * OB;
+            if (c < cols) {
+                if (OB == 4)
+                    reinterpret_cast<uint32_t*>(dst)[c] = *reinterpret_cast<const uint32_t*>(x);
+                else
+                    reinterpret_cast<uint16_t*>(dst)[c] = *reinterpret_cast<const uint16_t*>(x);
             }
         }
-        dst += kRows * p.ldo * OB;
     }
 }
 
@@ -1062,25 +1067,26 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 // 253 us). A tile starts in the middle of a 128-row group of exponents every other
 // time; the MMA then takes them from two columns on.
 //
-// A stage of the ring holds two blocks: a barrier round trip for each block alone took
-// the issuing warp as long as its MMAs do. 12 epilogue warps (warps 2-13) take 64
+// One warp loads A, another B (warp 2): a block's loads took one warp 340 cycles to
+// issue. 12 epilogue warps (3-14) take 64
 // columns each; a piece of 32 rows x 128 bytes leaves through a TMA store (store_piece
-// where the result's rows are not 16-byte aligned).
+// where the result's rows are not 16-byte aligned). The odd CTA's epilogue warps free
+// an accumulator on a barrier of their own, which the CTA's warp 1 passes on: an
+// arrival on the other CTA's barrier is a release to the cluster, which waited 2,000
+// cycles for a warp's stores.
 
 constexpr int kPairN = 192;
 constexpr int kPairEpiWarps = 12;
-constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
-constexpr int kPerStage = 2;
-constexpr int kStages2 = 3;
+constexpr int kPairThreads = 96 + 32 * kPairEpiWarps;
+constexpr int kStages2 = 6;
 constexpr int kTurnBytes2 = kPairEpiWarps * 32 * 128;
 constexpr int kCodeTileB2 = kPairN / 2 * 128;
 constexpr int kSf2 = 3 * kAtomBytes;
 constexpr int kCodes2 = kCodeTile + kCodeTileB2;  // codes of one block
-constexpr int kSmem2 = 1024 + 256 + kTurnBytes2 + kStages2 * kPerStage * (kCodes2 + kSf2);
-constexpr int kSfSlots2 = kStages2 * kPerStage;
+constexpr int kSmem2 = 1024 + 256 + kTurnBytes2 + kStages2 * (kCodes2 + kSf2);
 constexpr int kSfCols2 = 12;
 constexpr int kSfBase2 = 2 * kPairN;
-static_assert(kSmem2 <= 227 * 1024 && kSfBase2 + kSfSlots2 * kSfCols2 <= 512, "shared or tensor memory");
+static_assert(kSmem2 <= 227 * 1024 && kSfBase2 + kStages2 * kSfCols2 <= 512, "shared or tensor memory");
 
 // The address of `addr` (this CTA's shared memory) in the pair's even CTA.
 __device__ __forceinline__ uint32_t in_even_cta(uint32_t addr) {
@@ -1143,16 +1149,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
-    uint8_t* sB = sA + S * kPerStage * kCodeTile;
-    uint8_t* turn = sB + S * kPerStage * kCodeTileB2;
+    uint8_t* sB = sA + S * kCodeTile;
+    uint8_t* turn = sB + S * kCodeTileB2;
     uint8_t* sSf = turn + kTurnBytes2;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sSf + S * kPerStage * kSf2);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sSf + S * kSf2);
     uint64_t* full = bars;            // (even CTA) both CTAs' loads of a stage
     uint64_t* empty = bars + S;       // (each CTA) the MMAs are done with a stage
     uint64_t* tfull = bars + 2 * S;   // (each CTA) an accumulator is complete
-    uint64_t* tempty = tfull + 2;     // (even CTA) both CTAs have read an accumulator
-    uint64_t* drain = tfull + 4;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 5);
+    uint64_t* tempty = tfull + 2;     // (each CTA) its epilogue has read an accumulator
+    uint64_t* odd_empty = tfull + 4;  // (even CTA) so has the odd CTA's
+    uint64_t* drain = tfull + 6;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 7);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1165,12 +1172,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(smem_u32(&full[s]), kPerStage);
+            mbar_init(smem_u32(&full[s]), 2);  // a load of A, one of B
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&tfull[a]), 1);
-            mbar_init(smem_u32(&tempty[a]), 2 * kPairEpiWarps);
+            mbar_init(smem_u32(&tempty[a]), kPairEpiWarps);
+            mbar_init(smem_u32(&odd_empty[a]), 1);
         }
         mbar_init(smem_u32(drain), 1);
         *abort_flag = 0;
@@ -1191,8 +1199,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pdl_wait();
     pdl_release();
 
-    if (warp == 0) {
-        int stage = 0, part = 0;
+    if (warp == 0 || warp == 2) {
+        const bool loads_a = warp == 0;
+        int stage = 0;
         uint32_t phase = 0, armed = 0, armed_parity = 0;
         bool ok = true;
         for (int64_t t = first; t < tiles && ok; t += step) {
@@ -1200,51 +1209,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int am = 2 * m + (int)rank;  // this CTA's 128-row group of A
             const int sb = 3 * n / 2;          // the first 128-row group of the tile's rows of B
             for (int kb = 0; kb < p.nkb; ++kb) {
-                if (part == 0) {
-                    ok = wait_bar<true>(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    armed |= 1u << stage;
-                    armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                ok = wait_bar<true>(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
                 }
+                armed |= 1u << stage;
+                armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
                 if (elect_one()) {
-                    const int at = stage * kPerStage + part;
-                    if (rank == 0)
-                        mbar_expect_tx(smem_u32(&full[stage]), (uint32_t)(2 * (kCodes2 + ((kb & 3) == 0 ? kSf2 : 0))));
+                    uint8_t* sf = sSf + stage * kSf2;
                     const uint32_t fb = in_even_cta(smem_u32(&full[stage]));
-                    tma_load_pair(smem_u32(sA + at * kCodeTile), &tmA, kb * kBlock, am * 128, fb);
-                    tma_load_pair(smem_u32(sB + at * kCodeTileB2), &tmB, kb * kBlock,
-                                  n * kPairN + (int)rank * (kPairN / 2), fb);
-                    if ((kb & 3) == 0) {
-                        uint8_t* sf = sSf + at * kSf2;
-                        tma_load_pair(smem_u32(sf), &tmSA, 0, am * groups + (kb >> 2), fb);
-                        tma_load_pair(smem_u32(sf + kAtomBytes), &tmSB, 0, sb * groups + (kb >> 2), fb);
-                        tma_load_pair(smem_u32(sf + 2 * kAtomBytes), &tmSB, 0, (sb + 1) * groups + (kb >> 2), fb);
+                    if (loads_a) {
+                        if (rank == 0)
+                            mbar_expect_tx(smem_u32(&full[stage]),
+                                           (uint32_t)(2 * (kCodeTile + ((kb & 3) == 0 ? kAtomBytes : 0))));
+                        tma_load_pair(smem_u32(sA + stage * kCodeTile), &tmA, kb * kBlock, am * 128, fb);
+                        if ((kb & 3) == 0) tma_load_pair(smem_u32(sf), &tmSA, 0, am * groups + (kb >> 2), fb);
+                    } else {
+                        if (rank == 0)
+                            mbar_expect_tx(smem_u32(&full[stage]),
+                                           (uint32_t)(2 * (kCodeTileB2 + ((kb & 3) == 0 ? 2 * kAtomBytes : 0))));
+                        tma_load_pair(smem_u32(sB + stage * kCodeTileB2), &tmB, kb * kBlock,
+                                      n * kPairN + (int)rank * (kPairN / 2), fb);
+                        if ((kb & 3) == 0) {
+                            tma_load_pair(smem_u32(sf + kAtomBytes), &tmSB, 0, sb * groups + (kb >> 2), fb);
+                            tma_load_pair(smem_u32(sf + 2 * kAtomBytes), &tmSB, 0, (sb + 1) * groups + (kb >> 2), fb);
+                        }
                     }
                 }
                 __syncwarp();
-                if (++part == kPerStage) {
-                    part = 0;
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
         }
-        if (part > 0 && rank == 0 && elect_one())  // the last stage's missing blocks
-            for (; part < kPerStage; ++part) mbar_arrive(smem_u32(&full[stage]));
-        __syncwarp();
         // (the even CTA's barriers stand for both CTAs' loads; neither CTA leaves before
         // the other, see the end)
-        if (!ok && rank == 0 && lane == 0)
+        if (!ok && rank == 0 && lane == 0 && loads_a)
             for (int s = 0; s < S; ++s)
                 if (armed & (1u << s)) mbar_drain(smem_u32(&full[s]), (armed_parity >> s) & 1u, drain_limit);
     } else if (warp == 1) {
         if (rank == 0) {
-            int stage = 0, part = 0, slot = kSfSlots2 - 1;
+            int stage = 0, slot = S - 1;
             uint32_t phase = 0, span = 0;  // spans issued
             bool ok = true;
             const uint64_t desc0 = smem_desc(0u, 2ull, 1024u);
@@ -1252,23 +1259,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             for (int64_t t = first; t < tiles && ok; t += step) {
                 const int n = (int)(t % p.n_tiles);
                 for (int kb = 0; kb < p.nkb; ++kb) {
-                    if (kb % kSpan == 0)
-                        ok = wait_bar<true>(smem_u32(&tempty[span & 1u]), ((span >> 1) & 1u) ^ 1u, p.wait_limit,
-                                            p.status, abort_flag);
-                    if (part == 0)
-                        ok = ok && wait_bar<true>(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag);
+                    if (kb % kSpan == 0) {
+                        const uint32_t parity = ((span >> 1) & 1u) ^ 1u;
+                        ok = wait_bar(smem_u32(&tempty[span & 1u]), parity, p.wait_limit, p.status, abort_flag) &&
+                             wait_bar<true>(smem_u32(&odd_empty[span & 1u]), parity, p.wait_limit, p.status, abort_flag);
+                    }
+                    ok = ok && wait_bar<true>(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag);
                     if (!__all_sync(0xFFFFFFFFu, ok)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    if ((kb & 3) == 0 && ++slot == kSfSlots2) slot = 0;
-                    const int at = stage * kPerStage + part;
+                    if ((kb & 3) == 0 && ++slot == S) slot = 0;
                     const uint32_t sf = tmem_base + (uint32_t)(kSfBase2 + slot * kSfCols2);
                     const uint32_t sfb = sf + 4 + 2 * (n & 1);
-                    const uint32_t ssf = smem_u32(sSf + at * kSf2);
-                    const uint64_t ad = desc0 | (a_base + at * (kCodeTile >> 4));
-                    const uint64_t bd = desc0 | (b_base + at * (kCodeTileB2 >> 4));
+                    const uint32_t ssf = smem_u32(sSf + stage * kSf2);
+                    const uint64_t ad = desc0 | (a_base + stage * (kCodeTile >> 4));
+                    const uint64_t bd = desc0 | (b_base + stage * (kCodeTileB2 >> 4));
                     const uint32_t idesc = mm_idesc(256, kPairN, (uint32_t)(kb & 3));
                     const uint32_t acc = tmem_base + (span & 1u) * kPairN;
                     const bool last = kb % kSpan == kSpan - 1 || kb == p.nkb - 1;
@@ -1281,17 +1288,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         for (int kk = 0; kk < 4; ++kk)
                             umma_block8<2>(acc, ad + 2 * kk, bd + 2 * kk, idesc, sf, sfb,
                                            (uint32_t)((kb % kSpan) | kk));
-                        if (part == kPerStage - 1) commit_both(smem_u32(&empty[stage]));
+                        commit_both(smem_u32(&empty[stage]));
                         if (last) commit_both(smem_u32(&tfull[span & 1u]));
                     }
                     __syncwarp();
                     if (last) ++span;
-                    if (++part == kPerStage) {
-                        part = 0;
-                        if (++stage == S) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
                 }
             }
@@ -1301,9 +1305,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                              : "memory");
                 mbar_drain(smem_u32(drain), 0u, drain_limit);
             }
+        } else if (lane == 0) {
+            const int64_t spans = first < tiles ? (tiles - first + step - 1) / step * ((p.nkb + kSpan - 1) / kSpan) : 0;
+            for (int64_t i = 0; i < spans; ++i) {
+                if (!wait_bar(smem_u32(&tempty[i & 1]), (uint32_t)(i >> 1) & 1u, p.wait_limit, p.status, abort_flag)) break;
+                arrive_remote(in_even_cta(smem_u32(&odd_empty[i & 1])));
+            }
         }
     } else {
-        const int ew = warp - 2;
+        const int ew = warp - 3;
         const int q = warp & 3, third = ew >> 2;
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
         uint8_t* buf = turn + ew * 32 * 128;
@@ -1328,7 +1338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 for (int i = 0; i < 2; ++i) add_columns(tbase + 32 * i, sum[i]);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_remote(in_even_cta(smem_u32(&tempty[acc])));
+                if (lane == 0) mbar_arrive(smem_u32(&tempty[acc]));
                 ++span;
             }
             if (!ok) break;
