@@ -123,8 +123,10 @@ int b8_device(int dev, DeviceFacts* out) {
             !b8_smem_attribute(b8::k_block8_matmul<128, 2, true>, b8::MmCfg<128, true>::kSmem) ||
             !b8_smem_attribute(b8::k_block8_matmul<32, 4, true>, b8::MmCfg<32, true>::kSmem) ||
             !b8_smem_attribute(b8::k_block8_matmul<32, 2, true>, b8::MmCfg<32, true>::kSmem) ||
-            !b8_smem_attribute(b8::k_block8_matmul_pair<4>, b8::kSmem2) ||
-            !b8_smem_attribute(b8::k_block8_matmul_pair<2>, b8::kSmem2)) {
+            !b8_smem_attribute(b8::k_block8_matmul_pair<4, false>, b8::kSmem2) ||
+            !b8_smem_attribute(b8::k_block8_matmul_pair<2, false>, b8::kSmem2) ||
+            !b8_smem_attribute(b8::k_block8_matmul_pair<4, true>, b8::kSmem2Ast) ||
+            !b8_smem_attribute(b8::k_block8_matmul_pair<2, true>, b8::kSmem2Ast)) {
             cudaGetLastError();
             return fail(EM_E_CUDA, "cudaFuncSetAttribute failed");
         }
@@ -160,7 +162,7 @@ int b8_write(bool cols, const void* X_, int64_t n, int64_t ldx, const int64_t* s
         return EM_OK;
     }
     const int64_t row_tiles = (n + b8::ColTile<T>::kRows - 1) / b8::ColTile<T>::kRows;
-    const int grid = (int)std::min<int64_t>(row_tiles * nb, (int64_t)sms * 8);
+    const int grid = (int)std::min<int64_t>(row_tiles * nb, (int64_t)sms * kB8PerSm);
     CK(launch_k(true, b8::k_block8_write_cols<T>, dim3(grid), dim3(256), 0, st, X, (int)n, d, ldx,
                 b8::vector_width<T>(X, ldx), slots, first, claims, codes, scales, m->rows, pitch, b8::FastDiv((uint32_t)row_tiles), m->status));
     return EM_OK;
@@ -273,9 +275,16 @@ int b8_launch_matmul(const em_block8_t* a, int64_t na, const em_block8_t* b, int
         if (p.ldo * (int64_t)esz >= (1ll << 40)) p.vec_ok = 0;
         CUtensorMap tmOut = tmA;  // not used where the result's rows are not aligned
         if (p.vec_ok) CKR(b8_out_map(&tmOut, p, esz));
-        CK(launch_k(true, esz == 4 ? b8::k_block8_matmul_pair<4> : b8::k_block8_matmul_pair<2>,
-                    dim3((unsigned)(2 * std::min(t2, pairs))), dim3(b8::kPairThreads), b8::kSmem2, st, tmA, tmB, tmSA, tmSB,
-                    tmOut, p));
+        // A stationary where the MMAs of a tile outlast its stores (65,536 x 4,096: bf16
+        // results at d = 384 131 us, 136 without, at 768 204 and 217; fp32 at 768 251 and
+        // 264). Below that the stores count, and consecutive tiles on one pair spread the
+        // pairs' stores over memory (fp32 at d = 384 225 us, 191 without; bf16 at 256 123
+        // and 116).
+        const bool ast = p.nkb <= b8::kAstBlocks && 2 * p.nkb >= 3 * (int)esz;
+        auto* kernel = esz == 4 ? (ast ? b8::k_block8_matmul_pair<4, true> : b8::k_block8_matmul_pair<4, false>)
+                                : (ast ? b8::k_block8_matmul_pair<2, true> : b8::k_block8_matmul_pair<2, false>);
+        CK(launch_k(true, kernel, dim3((unsigned)(2 * std::min(t2, pairs))), dim3(b8::kPairThreads),
+                    ast ? b8::kSmem2Ast : b8::kSmem2, st, tmA, tmB, tmSA, tmSB, tmOut, p));
         return EM_OK;
     }
     p.m_tiles = (int)((na + 127) / 128);

@@ -380,8 +380,9 @@ __global__ void __launch_bounds__(256)
 // maxima (of 16-bit types two to a word) meet by shuffles and in shared memory; the
 // words are turned in shared memory (16-byte pieces of a row XORed with the row's group
 // of V, which keeps both sides off each other's banks) and leave as 128 bytes per row.
-// 64 registers, so that four blocks share an SM: with the values kept as floats it
-// took 100, and 46 us instead of 30 for 1,000 rows of 30,001 fp16 values.
+// 48 registers, so that five blocks share an SM, and a row's exponent is found by one
+// thread: 1,000 rows of 30,001 fp16 values take 19 us (with the values kept as floats,
+// 100 registers, and every thread finding the exponents 46).
 template <class T>
 struct ColTile {
     static constexpr int V = 16 / (int)sizeof(T);
@@ -391,7 +392,7 @@ struct ColTile {
 };
 
 template <class T>
-__global__ void __launch_bounds__(256, 4)
+__global__ void __launch_bounds__(256, 5)
     k_block8_write_cols(const T* __restrict__ X, int n, int d, int64_t ldx, int width,
                         const int64_t* __restrict__ slots, int64_t first, const int* __restrict__ claims,
                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t rows, int pitch,
@@ -400,6 +401,7 @@ __global__ void __launch_bounds__(256, 4)
     constexpr int V = C::V, kRows = C::kRows, PW = C::kPerWord;
     __shared__ __align__(16) uint32_t amax[8][kRows / PW];
     __shared__ __align__(16) uint8_t turned[kRows * kBlock];
+    __shared__ __align__(16) float inverse[kRows];  // 2^-e of the tile's rows
     __shared__ int dest[kRows];
     pdl_wait();
     pdl_release();
@@ -464,30 +466,26 @@ __global__ void __launch_bounds__(256, 4)
         }
         if (lane < 8) *reinterpret_cast<uint4*>(&amax[w][4 * k]) = make_uint4(a[0], a[1], a[2], a[3]);
         __syncthreads();
+        if (threadIdx.x < kRows / PW) {  // one thread per word of maxima: the rows' exponents
+            const int i = PW * threadIdx.x;
+            uint32_t m = amax[0][threadIdx.x];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) a[h] = 0u;
+            for (int q = 1; q < 8; ++q) m = max_parts<T>(m, amax[q][threadIdx.x]);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const uint4 f = *reinterpret_cast<const uint4*>(&amax[q][4 * k]);
-            a[0] = max_parts<T>(a[0], f.x);
-            a[1] = max_parts<T>(a[1], f.y);
-            a[2] = max_parts<T>(a[2], f.z);
-            a[3] = max_parts<T>(a[3], f.w);
+            for (int r = 0; r < PW; ++r) {
+                const int e = block_exponent(__float_as_uint(part_of<T>(m, r)));
+                inverse[i + r] = __uint_as_float((uint32_t)(127 - e) << 23);
+                const int to = slots ? dest[i + r] : base + i + r < n ? (int)first + base + i + r : -1;
+                if (to >= 0) scales[scale_at(to, b, groups)] = (uint8_t)(e + 127);
+            }
         }
-        int mine = 0;  // the exponent of row jq of the thread's V
+        __syncthreads();
 #pragma unroll
         for (int r = 0; r < V; ++r) {
-            const int e = block_exponent(__float_as_uint(part_of<T>(a[r / PW], r % PW)));
-            const float inverse = __uint_as_float((uint32_t)(127 - e) << 23);
             const float v[4] = {part_of<T>(x[0][r / PW], r % PW), part_of<T>(x[1][r / PW], r % PW),
                                 part_of<T>(x[2][r / PW], r % PW), part_of<T>(x[3][r / PW], r % PW)};
-            *reinterpret_cast<uint32_t*>(turned + (V * k + r) * kBlock + 4 * (jq ^ (4 * k))) = encode4(v, inverse);
-            mine = jq == r ? e : mine;
-        }
-        if (jq < V) {
-            const int i = i0 + jq;
-            const int to = slots ? dest[V * k + jq] : i < n ? (int)first + i : -1;
-            if (to >= 0) scales[scale_at(to, b, groups)] = (uint8_t)(mine + 127);
+            *reinterpret_cast<uint32_t*>(turned + (V * k + r) * kBlock + 4 * (jq ^ (4 * k))) =
+                encode4(v, inverse[V * k + r]);
         }
         __syncthreads();
         // 8 threads per row, 16 codes each
@@ -1074,6 +1072,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 // an accumulator on a barrier of their own, which the CTA's warp 1 passes on: an
 // arrival on the other CTA's barrier is a release to the cluster, which waited 2,000
 // cycles for a warp's stores.
+//
+// AST ("A stationary", rows of at most kAstBlocks blocks): a CTA takes consecutive
+// tiles, keeps its 128 rows of A in shared memory while their row of tiles lasts, and
+// streams only B: 12 KB a block instead of 28. L2 delivers about 61 bytes a cycle to an
+// SM, less than 28 KB in a block's 384 cycles.
 
 constexpr int kPairN = 192;
 constexpr int kPairEpiWarps = 12;
@@ -1083,10 +1086,13 @@ constexpr int kTurnBytes2 = kPairEpiWarps * 32 * 128;
 constexpr int kCodeTileB2 = kPairN / 2 * 128;
 constexpr int kSf2 = 3 * kAtomBytes;
 constexpr int kCodes2 = kCodeTile + kCodeTileB2;  // codes of one block
+constexpr int kAstBlocks = 6;
 constexpr int kSmem2 = 1024 + 256 + kTurnBytes2 + kStages2 * (kCodes2 + kSf2);
+constexpr int kSmem2Ast = 1024 + 256 + kTurnBytes2 + kAstBlocks * kCodeTile + (kAstBlocks + 3) / 4 * kAtomBytes +
+                          kStages2 * (kCodeTileB2 + 2 * kAtomBytes);
 constexpr int kSfCols2 = 12;
 constexpr int kSfBase2 = 2 * kPairN;
-static_assert(kSmem2 <= 227 * 1024 && kSfBase2 + kStages2 * kSfCols2 <= 512, "shared or tensor memory");
+static_assert(kSmem2 <= 227 * 1024 && kSmem2Ast <= 227 * 1024 && kSfBase2 + kStages2 * kSfCols2 <= 512, "shared or tensor memory");
 
 // The address of `addr` (this CTA's shared memory) in the pair's even CTA.
 __device__ __forceinline__ uint32_t in_even_cta(uint32_t addr) {
@@ -1102,6 +1108,13 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* t
         "%3}], [%4];" ::"r"(dst),
         "l"((uint64_t)tm), "r"(x), "r"(y), "r"(bar)
         : "memory");
+}
+
+// wait_bar by a whole warp, with one vote where the phase is complete already.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, long long limit, int* status,
+                                          volatile int* abort_flag) {
+    if (__all_sync(0xFFFFFFFFu, try_bar<true>(bar, parity))) return true;
+    return __all_sync(0xFFFFFFFFu, wait_bar<true>(bar, parity, limit, status, abort_flag));
 }
 
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
@@ -1139,7 +1152,7 @@ __device__ __forceinline__ void store_tma(const uint32_t (&w)[32], uint8_t* buf,
     }
 }
 
-template <int OB>
+template <int OB, bool AST>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_block8_matmul_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
@@ -1149,17 +1162,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
-    uint8_t* sB = sA + S * kCodeTile;
+    uint8_t* sB = sA + (AST ? kAstBlocks : S) * kCodeTile;
     uint8_t* turn = sB + S * kCodeTileB2;
-    uint8_t* sSf = turn + kTurnBytes2;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sSf + S * kSf2);
+    uint8_t* sSfA = turn + kTurnBytes2;  // exponents of A: a stage's, or (AST) the row of tiles'
+    uint8_t* sSfB = sSfA + (AST ? (kAstBlocks + 3) / 4 : S) * kAtomBytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sSfB + S * 2 * kAtomBytes);
     uint64_t* full = bars;            // (even CTA) both CTAs' loads of a stage
     uint64_t* empty = bars + S;       // (each CTA) the MMAs are done with a stage
     uint64_t* tfull = bars + 2 * S;   // (each CTA) an accumulator is complete
     uint64_t* tempty = tfull + 2;     // (each CTA) its epilogue has read an accumulator
     uint64_t* odd_empty = tfull + 4;  // (even CTA) so has the odd CTA's
     uint64_t* drain = tfull + 6;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 7);
+    uint64_t* afull = tfull + 7;      // (AST; even CTA) both CTAs' rows of A
+    uint64_t* aempty = tfull + 8;     // (AST; each CTA) the MMAs are done with them
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 9);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1167,12 +1183,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     const long long drain_limit = p.wait_limit > 4000000000ll ? p.wait_limit : 4000000000ll;
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
-    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    // this pair's tiles: every step-th, or (AST) consecutive ones
+    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int64_t first = AST ? pair * tiles / pairs : pair;
+    const int64_t end = AST ? (pair + 1) * tiles / pairs : tiles;
+    const int64_t step = AST ? 1 : pairs;
     const int groups = (p.nkb + 3) / 4;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(smem_u32(&full[s]), 2);  // a load of A, one of B
+            mbar_init(smem_u32(&full[s]), AST ? 1 : 2);  // a load of A, one of B
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -1181,6 +1201,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             mbar_init(smem_u32(&odd_empty[a]), 1);
         }
         mbar_init(smem_u32(drain), 1);
+        mbar_init(smem_u32(afull), 1);
+        mbar_init(smem_u32(aempty), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1199,32 +1221,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pdl_wait();
     pdl_release();
 
-    if (warp == 0 || warp == 2) {
+    if (AST && warp == 0) {
+        int last_m = -1;
+        uint32_t rows = 0;  // rows of tiles begun
+        bool ok = true;
+        for (int64_t t = first; t < end && ok; t += step) {
+            const int m = (int)(t / p.n_tiles);
+            if (m == last_m) continue;
+            last_m = m;
+            ok = wait_bar<true>(smem_u32(aempty), (rows & 1u) ^ 1u, p.wait_limit, p.status, abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            ++rows;
+            if (elect_one()) {
+                const int am = 2 * m + (int)rank;
+                if (rank == 0) mbar_expect_tx(smem_u32(afull), (uint32_t)(2 * (p.nkb * kCodeTile + groups * kAtomBytes)));
+                const uint32_t fb = in_even_cta(smem_u32(afull));
+                for (int kb = 0; kb < p.nkb; ++kb) tma_load_pair(smem_u32(sA + kb * kCodeTile), &tmA, kb * kBlock, am * 128, fb);
+                for (int g = 0; g < groups; ++g)
+                    tma_load_pair(smem_u32(sSfA + g * kAtomBytes), &tmSA, 0, am * groups + g, fb);
+            }
+            __syncwarp();
+        }
+        if (!ok && rank == 0 && lane == 0 && rows > 0) mbar_drain(smem_u32(afull), (rows - 1) & 1u, drain_limit);
+    } else if (warp == 0 || warp == 2) {
         const bool loads_a = warp == 0;
         int stage = 0;
         uint32_t phase = 0, armed = 0, armed_parity = 0;
         bool ok = true;
-        for (int64_t t = first; t < tiles && ok; t += step) {
+        for (int64_t t = first; t < end && ok; t += step) {
             const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
             const int am = 2 * m + (int)rank;  // this CTA's 128-row group of A
             const int sb = 3 * n / 2;          // the first 128-row group of the tile's rows of B
             for (int kb = 0; kb < p.nkb; ++kb) {
-                ok = wait_bar<true>(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag);
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    ok = false;
-                    break;
-                }
+                ok = wait_warp(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag);
+                if (!ok) break;
                 armed |= 1u << stage;
                 armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
                 if (elect_one()) {
-                    uint8_t* sf = sSf + stage * kSf2;
+                    uint8_t* sfb = sSfB + stage * 2 * kAtomBytes;
                     const uint32_t fb = in_even_cta(smem_u32(&full[stage]));
                     if (loads_a) {
                         if (rank == 0)
                             mbar_expect_tx(smem_u32(&full[stage]),
                                            (uint32_t)(2 * (kCodeTile + ((kb & 3) == 0 ? kAtomBytes : 0))));
                         tma_load_pair(smem_u32(sA + stage * kCodeTile), &tmA, kb * kBlock, am * 128, fb);
-                        if ((kb & 3) == 0) tma_load_pair(smem_u32(sf), &tmSA, 0, am * groups + (kb >> 2), fb);
+                        if ((kb & 3) == 0) tma_load_pair(smem_u32(sSfA + stage * kAtomBytes), &tmSA, 0, am * groups + (kb >> 2), fb);
                     } else {
                         if (rank == 0)
                             mbar_expect_tx(smem_u32(&full[stage]),
@@ -1232,8 +1274,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         tma_load_pair(smem_u32(sB + stage * kCodeTileB2), &tmB, kb * kBlock,
                                       n * kPairN + (int)rank * (kPairN / 2), fb);
                         if ((kb & 3) == 0) {
-                            tma_load_pair(smem_u32(sf + kAtomBytes), &tmSB, 0, sb * groups + (kb >> 2), fb);
-                            tma_load_pair(smem_u32(sf + 2 * kAtomBytes), &tmSB, 0, (sb + 1) * groups + (kb >> 2), fb);
+                            tma_load_pair(smem_u32(sfb), &tmSB, 0, sb * groups + (kb >> 2), fb);
+                            tma_load_pair(smem_u32(sfb + kAtomBytes), &tmSB, 0, (sb + 1) * groups + (kb >> 2), fb);
                         }
                     }
                 }
@@ -1246,57 +1288,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         // (the even CTA's barriers stand for both CTAs' loads; neither CTA leaves before
         // the other, see the end)
-        if (!ok && rank == 0 && lane == 0 && loads_a)
+        if (!ok && rank == 0 && lane == 0 && (AST || loads_a))
             for (int s = 0; s < S; ++s)
                 if (armed & (1u << s)) mbar_drain(smem_u32(&full[s]), (armed_parity >> s) & 1u, drain_limit);
     } else if (warp == 1) {
         if (rank == 0) {
             int stage = 0, slot = S - 1;
             uint32_t phase = 0, span = 0;  // spans issued
+            uint32_t rows = 0;             // (AST) rows of tiles begun
+            int last_m = -1;
             bool ok = true;
             const uint64_t desc0 = smem_desc(0u, 2ull, 1024u);
             const uint32_t a_base = smem_u32(sA) >> 4, b_base = smem_u32(sB) >> 4;
-            for (int64_t t = first; t < tiles && ok; t += step) {
-                const int n = (int)(t % p.n_tiles);
-                for (int kb = 0; kb < p.nkb; ++kb) {
-                    if (kb % kSpan == 0) {
+            for (int64_t t = first; t < end && ok; t += step) {
+                const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
+                if (AST && m != last_m) {
+                    last_m = m;
+                    ok = wait_warp(smem_u32(afull), rows & 1u, p.wait_limit, p.status, abort_flag);
+                    ++rows;
+                }
+                // four blocks share a group of exponents; unrolled, so that what the MMAs
+                // take but a block's stage is fixed
+                for (int kb0 = 0; kb0 < p.nkb && ok; kb0 += 4) {
+                    if (kb0 % kSpan == 0) {
                         const uint32_t parity = ((span >> 1) & 1u) ^ 1u;
-                        ok = wait_bar(smem_u32(&tempty[span & 1u]), parity, p.wait_limit, p.status, abort_flag) &&
-                             wait_bar<true>(smem_u32(&odd_empty[span & 1u]), parity, p.wait_limit, p.status, abort_flag);
+                        ok = wait_warp(smem_u32(&tempty[span & 1u]), parity, p.wait_limit, p.status, abort_flag) &&
+                             wait_warp(smem_u32(&odd_empty[span & 1u]), parity, p.wait_limit, p.status, abort_flag);
                     }
-                    ok = ok && wait_bar<true>(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if ((kb & 3) == 0 && ++slot == S) slot = 0;
+                    if (++slot == S) slot = 0;
                     const uint32_t sf = tmem_base + (uint32_t)(kSfBase2 + slot * kSfCols2);
                     const uint32_t sfb = sf + 4 + 2 * (n & 1);
-                    const uint32_t ssf = smem_u32(sSf + stage * kSf2);
-                    const uint64_t ad = desc0 | (a_base + stage * (kCodeTile >> 4));
-                    const uint64_t bd = desc0 | (b_base + stage * (kCodeTileB2 >> 4));
-                    const uint32_t idesc = mm_idesc(256, kPairN, (uint32_t)(kb & 3));
                     const uint32_t acc = tmem_base + (span & 1u) * kPairN;
-                    const bool last = kb % kSpan == kSpan - 1 || kb == p.nkb - 1;
-                    if (elect_one()) {
-                        if ((kb & 3) == 0) {
+                    const int blocks = min(4, p.nkb - kb0);
+                    const bool last = kb0 % kSpan + 4 == kSpan || kb0 + blocks == p.nkb;
 #pragma unroll
-                            for (int q = 0; q < 3; ++q) copy_exponents<2>(sf + 4 * q, ssf + q * kAtomBytes);
+                    for (int i = 0; i < 4; ++i) {
+                        if (i >= blocks) break;
+                        ok = ok && wait_warp(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t a_lo = a_base + (uint32_t)(AST ? kb0 + i : stage) * (kCodeTile >> 4);
+                        const uint32_t b_lo = b_base + (uint32_t)stage * (kCodeTileB2 >> 4);
+                        if (elect_one()) {
+                            if (i == 0) {
+                                copy_exponents<2>(sf, smem_u32(sSfA + (AST ? kb0 >> 2 : stage) * kAtomBytes));
+                                copy_exponents<2>(sf + 4, smem_u32(sSfB + stage * 2 * kAtomBytes));
+                                copy_exponents<2>(sf + 8, smem_u32(sSfB + (stage * 2 + 1) * kAtomBytes));
+                            }
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_block8<2>(acc, desc0 | (a_lo + 2 * kk), desc0 | (b_lo + 2 * kk),
+                                               mm_idesc(256, kPairN, (uint32_t)i), sf, sfb,
+                                               (i | kk) != 0 ? 1u : (uint32_t)(kb0 % kSpan));
+                            commit_both(smem_u32(&empty[stage]));
+                            if (last && i == blocks - 1) {
+                                commit_both(smem_u32(&tfull[span & 1u]));
+                                if (AST && kb0 + blocks == p.nkb && (t + 1 == end || n == p.n_tiles - 1))
+                                    commit_both(smem_u32(aempty));
+                            }
                         }
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_block8<2>(acc, ad + 2 * kk, bd + 2 * kk, idesc, sf, sfb,
-                                           (uint32_t)((kb % kSpan) | kk));
-                        commit_both(smem_u32(&empty[stage]));
-                        if (last) commit_both(smem_u32(&tfull[span & 1u]));
+                        __syncwarp();
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
-                    __syncwarp();
                     if (last) ++span;
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
                 }
             }
             if (!ok && elect_one()) {
@@ -1306,7 +1363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 mbar_drain(smem_u32(drain), 0u, drain_limit);
             }
         } else if (lane == 0) {
-            const int64_t spans = first < tiles ? (tiles - first + step - 1) / step * ((p.nkb + kSpan - 1) / kSpan) : 0;
+            const int64_t spans = first < end ? (end - first + step - 1) / step * ((p.nkb + kSpan - 1) / kSpan) : 0;
             for (int64_t i = 0; i < spans; ++i) {
                 if (!wait_bar(smem_u32(&tempty[i & 1]), (uint32_t)(i >> 1) & 1u, p.wait_limit, p.status, abort_flag)) break;
                 arrive_remote(in_even_cta(smem_u32(&odd_empty[i & 1])));
@@ -1319,7 +1376,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         uint8_t* buf = turn + ew * 32 * 128;
         uint32_t span = 0;
         bool ok = true;
-        for (int64_t t = first; t < tiles && ok; t += step) {
+        for (int64_t t = first; t < end && ok; t += step) {
             const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
             const int64_t row0 = (int64_t)m * 256 + rank * 128 + 32 * q;
             const int64_t col0 = (int64_t)n * kPairN + third * 64;
