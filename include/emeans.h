@@ -368,7 +368,8 @@ int em_sync(em_model* m);
 /* Exercises the failure path without a fault: which = 0 runs the search kernel's
  * bounded mbarrier wait on a barrier nothing arrives on, which gives up after
  * wait_ms and returns EM_E_TIMEOUT; which = 1 raises the index-check error and
- * returns EM_E_BOUNDS. The error word is cleared when reported, so the model stays
+ * returns EM_E_BOUNDS; which = 3 does as 0 with the wait of the block8 products, by
+ * two warps, of which one gives up because the other did. The error word is cleared when reported, so the model stays
  * usable. wait_ms in (0, 10000]. */
 int em_selftest(em_model* m, int which, double wait_ms);
 

@@ -487,7 +487,7 @@ class Model:
         return shift, float(sc.value)
 
     def selftest(self, which, wait_ms=200.0) -> int:
-        """Status of em_selftest (EM_E_TIMEOUT for which=0, EM_E_BOUNDS for which=1)."""
+        """Status of em_selftest (EM_E_TIMEOUT for which=0 and 3, EM_E_BOUNDS for which=1)."""
         return int(em_selftest(self.h, int(which), float(wait_ms)))
 
     def dp_world(self):

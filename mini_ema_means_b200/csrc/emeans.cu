@@ -2151,13 +2151,17 @@ int em_sync(em_model* m) {
 
 int em_selftest(em_model* m, int which, double wait_ms) {
     if (!m) return fail(EM_E_INVAL, "model is NULL");
-    if (which != 0 && which != 1) return fail(EM_E_INVAL, "which is 0 (bounded wait) or 1 (index check)");
+    if (which != 0 && which != 1 && which != 3)
+        return fail(EM_E_INVAL, "which is 0 (bounded wait), 1 (index check) or 3 (a block8 product's bounded wait)");
     if (!(wait_ms > 0.0 && wait_ms <= 10000.0)) return fail(EM_E_INVAL, "wait_ms must be in (0, 10000]");
     CKR(set_device(m));
     CKR(drop_prefetch(m));
     int clock_khz = 1965000;
     cudaDeviceGetAttribute(&clock_khz, cudaDevAttrClockRate, m->dev);
-    tc::k_selftest<<<1, 32, 0, m->stream>>>(which, (long long)(wait_ms * (double)clock_khz), m->err.p);
+    if (which == 3)
+        b8::k_block8_selftest<<<1, 64, 0, m->stream>>>((long long)(wait_ms * (double)clock_khz), m->err.p);
+    else
+        tc::k_selftest<<<1, 32, 0, m->stream>>>(which, (long long)(wait_ms * (double)clock_khz), m->err.p);
     CK(cudaGetLastError());
     EM_LAUNCHED(m, 1);
     return em_sync(m);

@@ -627,6 +627,21 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, long lon
     }
 }
 
+// Self-test of the failure path (em_selftest 3): two warps wait on a barrier that
+// nothing arrives on; one reaches its limit, the other sees the abort flag.
+__global__ void k_block8_selftest(long long limit, int* status) {
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ int abort_flag;
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        tc::mbar_init(tc::smem_u32(&bar), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    // the second warp's own limit is far beyond the first's
+    wait_bar<true>(tc::smem_u32(&bar), 0u, threadIdx.x < 32 ? limit : 64 * limit, status, &abort_flag);
+}
+
 // One lane of a converged warp. The issuing warps walk their loops with all lanes and
 // let one issue: the loop's values stay warp-uniform, and the MMA's operands with them
 // (under a branch on the lane the issue itself took longer than the MMAs).

@@ -115,6 +115,7 @@ def _cases(em):
         (_write, dict(v=v(status=(1 << 23) + 2))), (_write, dict(v=v(rows=0))), (_write, dict(v=v(d=0))),
         (_write, dict(dtype=3)), (_write, dict(dtype=-1)), (_write, dict(X=X + 2)), (_write, dict(X=X + 1, dtype=1)),
         (_write, dict(X=None)), (_write, dict(n=-1)), (_write, dict(n=1 << 31)), (_write, dict(first=-1)),
+        (_write, dict(v=v(rows=1 << 20, d=1 << 24), n=1 << 14)), (_read, dict(v=v(rows=1 << 20, d=1 << 24), n=1 << 14, rs=1 << 24)),
         (_write, dict(first=191)), (_write, dict(n=201)), (_write, dict(rs=130, cs=2)), (_write, dict(rs=-1, cs=1)),
         (_write, dict(first=1, slots=1 << 25)), (_write, dict(slots=(1 << 25) + 4)),
         (_write, dict(v=v(claims=None), n=600, slots=1 << 25)),

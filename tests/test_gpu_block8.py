@@ -108,6 +108,30 @@ def test_special_values(em):
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("d", [136, 141])
+def test_non_finite_values_leave_their_neighbours_alone(em, kind, d):
+    """NaN and infinities of both signs in every place of a row's two blocks, whole blocks
+    of them, and rows without any in between."""
+    x = _rows(2 * d + 3, d, 17, kind)
+    inf, nan = float("inf"), float("nan")
+    for i in range(d):
+        x[2 * i, i] = (inf, -inf, nan)[i % 3]
+    x[2 * d] = nan
+    x[2 * d + 1, :128], x[2 * d + 1, 128:] = inf, 1.0
+    x[2 * d + 2, 128:] = -inf
+    for xin in (x.cuda(), x.cuda().t().contiguous().t()):
+        m = em.Block8(len(x), d)
+        m.write(xin)
+        _check_rows(m, np.arange(len(x)), x)
+        for out_kind, dt in TYPES.items():
+            out = torch.empty(len(x), d, dtype=dt, device="cuda")
+            m.read(out)
+            ref = torch.from_numpy(B.held(_f64(x))).to(dt)
+            assert torch.equal(torch.isnan(out.cpu()), ~torch.isfinite(x))
+            assert torch.equal(out.cpu().nan_to_num(0.0), ref.nan_to_num(0.0)), out_kind
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
 def test_strides_and_alignments(em, kind):
     """Pitched, offset, repeated and transposed inputs, and outputs off every vector width."""
     big = _rows(40, 300, 5, kind).cuda()
@@ -232,6 +256,45 @@ def test_product(em, na, nb, d, kind):
         A.check()
         _assert_product(wide[1:na + 1, :nb], B.held(_f64(x)), B.held(_f64(y)), kind)
         assert (wide[0] == 5).all() and (wide[na + 1] == 5).all() and (wide[:, nb:] == 5).all()
+
+
+# More than a wave of 128 x 128 tiles: pairs of CTAs. Rows of 3 to 6 blocks (A kept),
+# more and fewer, ragged in both directions, one span and several.
+LARGE = [(2500, 1500, 300), (1500, 3001, 700), (20000, 777, 96), (2100, 2000, 1300), (1300, 2050, 2100), (1921, 1729, 640)]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("na,nb,d", LARGE)
+def test_large_product(em, na, nb, d, kind):
+    x, y = _plain(na, d, 1), _plain(nb, d, 2)
+    A, Bm = em.Block8(na + 5, d), em.Block8(nb + 200, d)
+    for m, v in ((A, x), (Bm, y)):
+        m.codes.fill_(0x7F)
+        m.scales.fill_(0xFF)
+        m.write(v.cuda())
+    a, b = B.held(_f64(x)), B.held(_f64(y))
+    for pad in (0, 1, 8):
+        wide = torch.full((na + 2, nb + pad), 5.0, dtype=TYPES[kind], device="cuda")
+        A.matmul(Bm, wide[1:na + 1, :nb])
+        A.check()
+        _assert_product(wide[1:na + 1, :nb], a, b, kind)
+        assert (wide[0] == 5).all() and (wide[na + 1] == 5).all() and (wide[:, nb:] == 5).all()
+
+
+def test_one_row_of_results_is_the_same_whoever_computes_it(em):
+    """Few rows, some and many take different kernels; the sums of a result are the
+    same in each, bit for bit."""
+    d = 900
+    x, y = _plain(2000, d, 1), _plain(1700, d, 2)
+    A, Bm = em.Block8(2000, d), em.Block8(1700, d)
+    A.write(x.cuda())
+    Bm.write(y.cuda())
+    all_rows = torch.empty(2000, 1700, device="cuda")
+    A.matmul(Bm, all_rows)
+    for n in (1, 20, 32, 33, 128, 129, 300):
+        out = torch.empty(n, 1700, device="cuda")
+        A.matmul(Bm, out)
+        assert torch.equal(out, all_rows[:n]), n
 
 
 def test_product_of_a_matrix_with_itself_and_repeats(em):
@@ -452,6 +515,23 @@ def test_offsets_past_32_bits(em):
     m.matmul(em.Block8(3, d), wide)
     m.check()
     assert (wide == 0).all()
+
+
+def test_a_wait_that_runs_out_is_reported(em):
+    """The bounded wait of the products: gives up within its limit, leaves the context
+    usable, and one warp's giving up ends the other's wait."""
+    import time
+
+    m = em.Model(8, 4, seed=1)
+    t0 = time.monotonic()
+    assert m.selftest(3, wait_ms=200.0) == em.EM_E_TIMEOUT
+    assert time.monotonic() - t0 < 5.0  # the second warp alone would wait 12.8 s
+    m.close()
+    a = em.Block8(200, 64)
+    out = torch.ones(200, 200, device="cuda")
+    a.matmul(a, out)
+    a.check()
+    assert (out == 0).all()
 
 
 # ---------------------------------------------------------------- with the model
