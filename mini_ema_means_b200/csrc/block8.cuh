@@ -172,14 +172,18 @@ template <class T>
 int b8_read_as(const em_block8_t* m, int64_t first, const int64_t* slots, int64_t n, void* out, int64_t ldo,
                int64_t columns, int sms, cudaStream_t st) {
     const int64_t nb = b8_blocks(m->d);
-    const int width = b8::vector_width<T>(out, ldo);
-    const bool fast = width * sizeof(T) == 16 && m->d % 8 == 0 && columns == m->d;
-    auto* kernel = slots ? (fast ? b8::k_block8_read<T, true, true> : b8::k_block8_read<T, true, false>)
-                         : (fast ? b8::k_block8_read<T, false, true> : b8::k_block8_read<T, false, false>);
-    CK(launch_k(true, kernel, dim3(b8_pair_grid(n, nb, sms)), dim3(256), 0, st,
-                static_cast<const uint8_t*>(m->codes), static_cast<const uint8_t*>(m->scales), m->rows,
-                (int)b8_pitch(m->d), (int)m->d, slots, (int)first, (int)n, static_cast<T*>(out), ldo, (int)columns, width,
-                b8::FastDiv((uint32_t)nb), m->status));
+    const dim3 grid(b8_pair_grid(n, nb, sms));
+    const auto codes = static_cast<const uint8_t*>(m->codes), scales = static_cast<const uint8_t*>(m->scales);
+    T* rows_out = static_cast<T*>(out);
+    if (columns == m->d && m->d % 16 == 0 && (uintptr_t)out % 32 == 0 && ldo * sizeof(T) % 32 == 0) {
+        CK(launch_k(true, slots ? b8::k_block8_read_wide<T, true> : b8::k_block8_read_wide<T, false>, grid, dim3(256), 0,
+                    st, codes, scales, m->rows, (int)m->d, slots, (int)first, (int)n, rows_out, ldo,
+                    b8::FastDiv((uint32_t)nb), m->status));
+        return EM_OK;
+    }
+    CK(launch_k(true, slots ? b8::k_block8_read<T, true> : b8::k_block8_read<T, false>, grid, dim3(256), 0, st, codes,
+                scales, m->rows, (int)b8_pitch(m->d), (int)m->d, slots, (int)first, (int)n, rows_out, ldo, (int)columns,
+                b8::vector_width<T>(out, ldo), b8::FastDiv((uint32_t)nb), m->status));
     return EM_OK;
 }
 

@@ -170,10 +170,10 @@ __device__ __forceinline__ int64_t slot_of(const int64_t* __restrict__ slots, in
 // Several rows of one call may name the same slot: the last of them stays, whole.
 // Calls of up to kScanRows rows look for a later row with the same slot where they
 // write; longer calls run this pass first, which leaves in claims[slot] the last row
-// of this call that names it. An entry from an earlier call counts only if that row
-// of this call names the slot too, so the array needs no initial value, and a
-// captured call can be replayed at any time. The loop ends: an entry is replaced by a
-// valid one or by a later row, at most once for each row that names the slot.
+// of this call that names it. Whoever takes a later row's place there puts it back: an
+// entry that this call did not make (its row does not name the slot) is no row of this
+// call, so the array needs no initial value, and a captured call can be replayed at any
+// time. The loop ends, since what it puts back grows.
 constexpr int kScanRows = 512;
 
 __global__ void k_block8_claim(const int64_t* __restrict__ slots, int64_t n, int64_t rows, int* __restrict__ claims) {
@@ -182,13 +182,10 @@ __global__ void k_block8_claim(const int64_t* __restrict__ slots, int64_t n, int
     for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t s = slots[i];
         if (s < 0 || s >= rows) continue;
-        int cur = *(volatile int*)(claims + s);
-        for (;;) {
-            const bool valid = cur >= 0 && cur < n && slots[cur] == s;
-            if (valid && cur >= (int)i) break;
-            const int seen = atomicCAS(claims + s, cur, (int)i);
-            if (seen == cur) break;
-            cur = seen;
+        for (int mine = (int)i;;) {
+            const int old = atomicExch(claims + s, mine);
+            if (old <= mine || old >= n || slots[old] != s) break;
+            mine = old;
         }
     }
 }
@@ -507,7 +504,7 @@ __global__ void __launch_bounds__(256, 5)
 // What bounds it is issue: 8 values are 27 instructions to load, decode, scale and
 // store, and finding them must not cost as much again (32-bit row numbers, the next
 // pair by steps, no branch between the loads).
-template <class T, bool SLOTS, bool FAST>
+template <class T, bool SLOTS>
 __global__ void __launch_bounds__(256, 5)
     k_block8_read(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int pitch,
                   int d, const int64_t* __restrict__ slots, int first, int n, T* __restrict__ out, int64_t ldo,
@@ -547,14 +544,83 @@ __global__ void __launch_bounds__(256, 5)
 #pragma unroll
             for (int t = 0; t < 8; ++t) v[t] *= scale;
             T* dst = out + (int64_t)at.row[s] * ldo + col;
-            if (FAST) {  // (columns = d, a multiple of 8, and 16-byte aligned rows)
-                if (col < d) store8_as<T, 16 / sizeof(T)>(dst, v);
-            } else {
-                if (col + 8 > d) {
+            if (col + 8 > d) {
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) v[t] = col + t < d ? v[t] : 0.0f;
+                for (int t = 0; t < 8; ++t) v[t] = col + t < d ? v[t] : 0.0f;
+            }
+            store8(dst, columns - col, width, v);
+        }
+    }
+}
+
+// The same where d is a multiple of 16 and the output's rows are 32-byte aligned: 16
+// values per lane, 8 lanes per pair, two steps of four pairs in flight, and 32-byte
+// stores. A lane's work to find its values is shared by twice as many.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+template <class T, bool SLOTS>
+__global__ void __launch_bounds__(256, 5)
+    k_block8_read_wide(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int d,
+                       const int64_t* __restrict__ slots, int first, int n, T* __restrict__ out, int64_t ldo, FastDiv nb,
+                       int* status) {
+    pdl_wait();
+    pdl_release();
+    constexpr int kWideSteps = 2;
+    static_assert(4 * kWideSteps == kPairsPerWarp, "the launch shape of k_block8_read");
+    const int lane = threadIdx.x & 31, part = lane >> 3, col16 = (lane & 7) * 16;
+    const uint32_t total = (uint32_t)n * nb.div;
+    const uint32_t stride = gridDim.x * (blockDim.x >> 5) * kPairsPerWarp;
+    const int groups = (int)(nb.div + 3) / 4;
+    for (uint32_t f0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kPairsPerWarp; f0 < total; f0 += stride) {
+        uint4 c[kWideSteps];
+        uint8_t byte[kWideSteps];
+        int row[kWideSteps], b[kWideSteps], from[kWideSteps];
+#pragma unroll
+        for (int s = 0; s < kWideSteps; ++s) {
+            const uint32_t f = f0 + 4 * s + part;
+            row[s] = (int)nb.quotient(f);
+            b[s] = (int)(f - (uint32_t)row[s] * nb.div);
+            from[s] = -1;
+            if (f < total) from[s] = SLOTS ? (int)slot_of(slots, 0, row[s], rows, status) : first + row[s];
+        }
+#pragma unroll
+        for (int s = 0; s < kWideSteps; ++s) {  // (as in k_block8_read: no branch parts the loads; d is the pitch)
+            const int r = max(from[s], 0);
+            c[s] = *reinterpret_cast<const uint4*>(codes + (int64_t)r * d + min(b[s] * kBlock + col16, d - 16));
+            byte[s] = scales[scale_at(r, b[s], groups)];
+        }
+#pragma unroll
+        for (int s = 0; s < kWideSteps; ++s) {
+            const int col = b[s] * kBlock + col16;
+            if (f0 + 4 * s + part >= total || col >= d) continue;
+            if (from[s] < 0) c[s] = make_uint4(0u, 0u, 0u, 0u);
+            const float scale = scale_of(byte[s]);
+            const uint32_t cw[4] = {c[s].x, c[s].y, c[s].z, c[s].w};
+            uint32_t w[8];
+            T* dst = out + (int64_t)row[s] * ldo + col;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[4];
+                decode4(cw[q], v);
+                if (sizeof(T) == 4) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) w[4 * (q & 1) + t] = __float_as_uint(v[t] * scale);
+                    if (q & 1) store32(dst + 8 * (q >> 1), w);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 4; t += 2) {
+                        const T lo = from_f32<T>(v[t] * scale), hi = from_f32<T>(v[t + 1] * scale);
+                        uint16_t l, h;
+                        memcpy(&l, &lo, 2);
+                        memcpy(&h, &hi, 2);
+                        w[2 * q + t / 2] = (uint32_t)l | ((uint32_t)h << 16);
+                    }
+                    if (q == 3) store32(dst, w);
                 }
-                store8(dst, columns - col, width, v);
             }
         }
     }
@@ -575,18 +641,18 @@ __global__ void __launch_bounds__(256, 5)
 // the epilogue adds the spans in order, rounding to nearest, in registers. Two
 // accumulators let it read one while the next span runs.
 //
-// Roles of a CTA's 10 warps:
-//   warp 0     one thread loads 128-byte-wide tiles of codes (TMA, 128-byte swizzle)
-//              and the exponents of their rows into a ring of stages
+// Roles of a CTA's warps:
+//   warps 0, 2 load A and B: 128-byte-wide tiles of codes (TMA, 128-byte swizzle) and
+//              the exponents of their rows into a ring of stages (one warp for both took
+//              a block's loads as long to issue as its MMAs run)
 //   warp 1     one thread issues the MMAs and, at every fourth block of a row, copies the
 //              exponents of four blocks to tensor memory. They go round as many sets of
 //              columns there as the ring has blocks: a set's last user is at least that
 //              many blocks back, and the wait for this block's stage was a wait for it
-//   warps 2-9  epilogue: two groups of four warps (one per TMEM lane quadrant) take
-//              the left and right half of a tile's columns
+//   from 3 on  epilogue: groups of four warps, one per TMEM lane quadrant, each with its
+//              columns of a tile
 
-constexpr int kMmThreads = 320;
-constexpr int kMmEpi = 256;
+constexpr int kMmThreads = 352;
 constexpr int kSpan = 8;                      // blocks of 128 values per accumulator
 constexpr int kTurnBytes = 8 * 32 * 128;      // epilogue warps' turning buffers
 constexpr int kCodeTile = 128 * 128;          // codes of 128 rows x one block
@@ -625,6 +691,14 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, long lon
             }
         }
     }
+}
+
+// wait_bar by a whole warp, with one vote where the phase is complete already.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, long long limit, int* status,
+                                          volatile int* abort_flag) {
+    if (__all_sync(0xFFFFFFFFu, try_bar<CLUSTER>(bar, parity))) return true;
+    return __all_sync(0xFFFFFFFFu, wait_bar<CLUSTER>(bar, parity, limit, status, abort_flag));
 }
 
 // Self-test of the failure path (em_selftest 3): two warps wait on a barrier that
@@ -874,7 +948,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(smem_u32(&full[s]), PER);
+            mbar_init(smem_u32(&full[s]), 2 * PER);  // a load of A, one of B, for each block
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int a = 0; a < ACC; ++a) {
@@ -899,7 +973,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     pdl_wait();
     pdl_release();
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 2) {
+        const bool loads_a = warp == 0;
         int stage = 0, part = 0;  // the next block's stage, and its place there
         uint32_t phase = 0, armed = 0, armed_parity = 0;
         bool ok = true;
@@ -907,24 +982,23 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
             for (int kb = 0; kb < p.nkb; ++kb) {
                 if (part == 0) {
-                    ok = wait_bar(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = wait_warp(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag);
+                    if (!ok) break;
                     armed |= 1u << stage;
                     armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
                 }
                 if (elect_one()) {
                     const uint32_t fb = smem_u32(&full[stage]);
                     const int at = stage * PER + part;
-                    mbar_expect_tx(fb, (uint32_t)(C::kCodes + ((kb & 3) == 0 ? C::kSf : 0)));
-                    tma_load_2d(smem_u32(sA + at * kCodeTile), &tmA, kb * kBlock, m * 128, fb);
-                    tma_load_2d(smem_u32(sB + at * C::kBTile), &tmB, kb * kBlock, n * BN, fb);
-                    if ((kb & 3) == 0) {
-                        uint8_t* sf = sSf + at * C::kSf;
-                        tma_load_2d(smem_u32(sf), &tmSA, 0, m * groups + (kb >> 2), fb);
-                        tma_load_2d(smem_u32(sf + kAtomBytes), &tmSB, 0, n * groups + (kb >> 2), fb);
+                    uint8_t* sf = sSf + at * C::kSf;
+                    if (loads_a) {
+                        mbar_expect_tx(fb, (uint32_t)(kCodeTile + ((kb & 3) == 0 ? kAtomBytes : 0)));
+                        tma_load_2d(smem_u32(sA + at * kCodeTile), &tmA, kb * kBlock, m * 128, fb);
+                        if ((kb & 3) == 0) tma_load_2d(smem_u32(sf), &tmSA, 0, m * groups + (kb >> 2), fb);
+                    } else {
+                        mbar_expect_tx(fb, (uint32_t)(C::kBTile + ((kb & 3) == 0 ? kAtomBytes : 0)));
+                        tma_load_2d(smem_u32(sB + at * C::kBTile), &tmB, kb * kBlock, n * BN, fb);
+                        if ((kb & 3) == 0) tma_load_2d(smem_u32(sf + kAtomBytes), &tmSB, 0, n * groups + (kb >> 2), fb);
                     }
                 }
                 __syncwarp();
@@ -940,7 +1014,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         if (part > 0 && elect_one())  // the last stage's missing blocks
             for (; part < PER; ++part) mbar_arrive(smem_u32(&full[stage]));
         __syncwarp();
-        if (!ok && lane == 0)
+        if (!ok && lane == 0 && loads_a)
             for (int s = 0; s < S; ++s)
                 if (armed & (1u << s)) mbar_drain(smem_u32(&full[s]), (armed_parity >> s) & 1u, drain_limit);
     } else if (warp == 1) {
@@ -950,48 +1024,50 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         const uint64_t desc0 = smem_desc(0u, 2ull, 1024u);
         const uint32_t a_base = smem_u32(sA) >> 4, b_base = smem_u32(sB) >> 4;
         for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            for (int kb = 0; kb < p.nkb; ++kb) {
-                if (kb % kSpan == 0)
-                    ok = wait_bar(smem_u32(&tempty[acc]), acc_phase ^ 1u, p.wait_limit, p.status, abort_flag);
-                if (part == 0)
-                    ok = ok && wait_bar(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag);
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if ((kb & 3) == 0 && ++slot == C::kSfSlots) slot = 0;
-                const int at = stage * PER + part;
+            // four blocks share a group of exponents; unrolled, so that what the MMAs take
+            // but a block's stage is fixed
+            for (int kb0 = 0; kb0 < p.nkb && ok; kb0 += 4) {
+                if (kb0 % kSpan == 0)
+                    ok = wait_warp(smem_u32(&tempty[acc]), acc_phase ^ 1u, p.wait_limit, p.status, abort_flag);
+                if (++slot == C::kSfSlots) slot = 0;
                 const uint32_t sf = tmem_base + (uint32_t)(C::kSfBase + slot * C::kSfCols);
-                const uint32_t ssf = smem_u32(sSf + at * C::kSf);
-                const uint64_t ad = desc0 | (a_base + at * (kCodeTile >> 4));
-                const uint64_t bd = desc0 | (b_base + at * (C::kBTile >> 4));
-                const uint32_t idesc = mm_idesc(128, BN, (uint32_t)(kb & 3));
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-                const bool last = kb % kSpan == kSpan - 1 || kb == p.nkb - 1;
-                if (elect_one()) {
-                    if ((kb & 3) == 0) {
-                        copy_exponents<1>(sf, ssf);
-                        copy_exponents<1>(sf + 4, ssf + kAtomBytes);
-                    }
+                const int blocks = min(4, p.nkb - kb0);
+                const bool last = kb0 % kSpan + 4 == kSpan || kb0 + blocks == p.nkb;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_block8<1>(d_tmem, ad + 2 * kk, bd + 2 * kk, idesc, sf, sf + 4,
-                                       (uint32_t)((kb % kSpan) | kk));
-                    if (part == PER - 1) umma_commit(smem_u32(&empty[stage]));
-                    if (last) umma_commit(smem_u32(&tfull[acc]));
+                for (int i = 0; i < 4; ++i) {
+                    if (i >= blocks) break;
+                    if (part == 0)
+                        ok = ok && wait_warp(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t at = (uint32_t)(stage * PER + part);
+                    const uint32_t a_lo = a_base + at * (kCodeTile >> 4), b_lo = b_base + at * (C::kBTile >> 4);
+                    if (elect_one()) {
+                        if (i == 0) {
+                            copy_exponents<1>(sf, smem_u32(sSf + at * C::kSf));
+                            copy_exponents<1>(sf + 4, smem_u32(sSf + at * C::kSf + kAtomBytes));
+                        }
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_block8<1>(d_tmem, desc0 | (a_lo + 2 * kk), desc0 | (b_lo + 2 * kk),
+                                           mm_idesc(128, BN, (uint32_t)i), sf, sf + 4,
+                                           (i | kk) != 0 ? 1u : (uint32_t)(kb0 % kSpan));
+                        if (part == PER - 1) umma_commit(smem_u32(&empty[stage]));
+                        if (last && i == blocks - 1) umma_commit(smem_u32(&tfull[acc]));
+                    }
+                    __syncwarp();
+                    if (++part == PER) {
+                        part = 0;
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
                 }
-                __syncwarp();
                 if (last && ++acc == ACC) {
                     acc = 0;
                     acc_phase ^= 1u;
-                }
-                if (++part == PER) {
-                    part = 0;
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
                 }
             }
         }
@@ -1000,7 +1076,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             mbar_drain(smem_u32(drain), 0u, drain_limit);
         }
     } else {
-        const int ew = warp - 2;
+        const int ew = warp - 3;
         const int q = warp & 3, half = ew >> 2;
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
         constexpr int kCols = C::kTurns ? BN : BN / 2;  // columns a warp takes
@@ -1018,8 +1094,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             clear_sums(sum);
             for (int s = 0; s < spans; ++s) {
                 const int acc = (int)(span % ACC);
-                if (!__all_sync(0xFFFFFFFFu, wait_bar(smem_u32(&tfull[acc]), (uint32_t)(span / ACC) & 1u, p.wait_limit,
-                                                      p.status, abort_flag))) {
+                if (!wait_warp(smem_u32(&tfull[acc]), (uint32_t)(span / ACC) & 1u, p.wait_limit, p.status, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -1123,13 +1198,6 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* t
         "%3}], [%4];" ::"r"(dst),
         "l"((uint64_t)tm), "r"(x), "r"(y), "r"(bar)
         : "memory");
-}
-
-// wait_bar by a whole warp, with one vote where the phase is complete already.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, long long limit, int* status,
-                                          volatile int* abort_flag) {
-    if (__all_sync(0xFFFFFFFFu, try_bar<true>(bar, parity))) return true;
-    return __all_sync(0xFFFFFFFFu, wait_bar<true>(bar, parity, limit, status, abort_flag));
 }
 
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
@@ -1269,7 +1337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int am = 2 * m + (int)rank;  // this CTA's 128-row group of A
             const int sb = 3 * n / 2;          // the first 128-row group of the tile's rows of B
             for (int kb = 0; kb < p.nkb; ++kb) {
-                ok = wait_warp(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag);
+                ok = wait_warp<true>(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag);
                 if (!ok) break;
                 armed |= 1u << stage;
                 armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
@@ -1319,7 +1387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
                 if (AST && m != last_m) {
                     last_m = m;
-                    ok = wait_warp(smem_u32(afull), rows & 1u, p.wait_limit, p.status, abort_flag);
+                    ok = wait_warp<true>(smem_u32(afull), rows & 1u, p.wait_limit, p.status, abort_flag);
                     ++rows;
                 }
                 // four blocks share a group of exponents; unrolled, so that what the MMAs
@@ -1327,8 +1395,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 for (int kb0 = 0; kb0 < p.nkb && ok; kb0 += 4) {
                     if (kb0 % kSpan == 0) {
                         const uint32_t parity = ((span >> 1) & 1u) ^ 1u;
-                        ok = wait_warp(smem_u32(&tempty[span & 1u]), parity, p.wait_limit, p.status, abort_flag) &&
-                             wait_warp(smem_u32(&odd_empty[span & 1u]), parity, p.wait_limit, p.status, abort_flag);
+                        ok = wait_warp<true>(smem_u32(&tempty[span & 1u]), parity, p.wait_limit, p.status, abort_flag) &&
+                             wait_warp<true>(smem_u32(&odd_empty[span & 1u]), parity, p.wait_limit, p.status, abort_flag);
                     }
                     if (++slot == S) slot = 0;
                     const uint32_t sf = tmem_base + (uint32_t)(kSfBase2 + slot * kSfCols2);
@@ -1339,7 +1407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if (i >= blocks) break;
-                        ok = ok && wait_warp(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag);
+                        ok = ok && wait_warp<true>(smem_u32(&full[stage]), phase, p.wait_limit, p.status, abort_flag);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t a_lo = a_base + (uint32_t)(AST ? kb0 + i : stage) * (kCodeTile >> 4);
@@ -1399,8 +1467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             clear_sums(sum);
             for (int kb = 0; kb < p.nkb; kb += kSpan) {
                 const uint32_t acc = span & 1u;
-                if (!__all_sync(0xFFFFFFFFu, wait_bar<true>(smem_u32(&tfull[acc]), (span >> 1) & 1u, p.wait_limit,
-                                                            p.status, abort_flag))) {
+                if (!wait_warp<true>(smem_u32(&tfull[acc]), (span >> 1) & 1u, p.wait_limit, p.status, abort_flag)) {
                     ok = false;
                     break;
                 }
