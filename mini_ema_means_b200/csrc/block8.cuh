@@ -153,6 +153,12 @@ int b8_write(bool cols, const void* X_, int64_t n, int64_t ldx, const int64_t* s
     const int64_t nb = b8_blocks(m->d);
     const int d = (int)m->d, pitch = (int)b8_pitch(m->d);
     if (!cols) {
+        if (d % 16 == 0 && (uintptr_t)X % 32 == 0 && ldx * sizeof(T) % 32 == 0) {
+            CK(launch_k(true, slots ? b8::k_block8_write_wide<T, true> : b8::k_block8_write_wide<T, false>,
+                        dim3(b8_pair_grid(n, nb, sms)), dim3(256), 0, st, X, (int)n, d, ldx, slots, (int)first, claims,
+                        codes, scales, m->rows, b8::FastDiv((uint32_t)nb), m->status));
+            return EM_OK;
+        }
         const int width = b8::vector_width<T>(X, ldx);
         const bool fast = width * sizeof(T) == 16 && d % 8 == 0;
         auto* kernel = slots ? (fast ? b8::k_block8_write<T, true, true> : b8::k_block8_write<T, true, false>)

@@ -190,7 +190,7 @@ __global__ void k_block8_claim(const int64_t* __restrict__ slots, int64_t n, int
     }
 }
 
-// Whether row i is the one that stays in its slot s. `lanes` (16 or 32) neighbouring
+// Whether row i is the one that stays in its slot s. `lanes` (8, 16 or 32) neighbouring
 // lanes ask for the same row, `lane` is this one's place among them; all lanes of the
 // warp call it together.
 __device__ __forceinline__ bool last_of_slot(const int64_t* __restrict__ slots, const int* __restrict__ claims,
@@ -201,7 +201,7 @@ __device__ __forceinline__ bool last_of_slot(const int64_t* __restrict__ slots, 
         for (int64_t j = i + 1 + lane; j < n; j += lanes) later |= slots[j] == s;
     const uint32_t all = __ballot_sync(0xFFFFFFFFu, later);
     const int shift = threadIdx.x & 31 & ~(lanes - 1);
-    return ((all >> shift) & (lanes == 32 ? 0xFFFFFFFFu : 0xFFFFu)) == 0u;
+    return ((all >> shift) & (0xFFFFFFFFu >> (32 - lanes))) == 0u;
 }
 
 // Words of magnitudes: the larger of each part; NaN gives way.
@@ -265,20 +265,28 @@ struct Pairs {
     }
 };
 
-// 8 values of type T as words; FAST: one or two 16-byte loads.
-template <class T>
-struct Eight {
-    static constexpr int kWords = 2 * (int)sizeof(T), PW = 4 / (int)sizeof(T);
+// N values of type T as words.
+template <class T, int N>
+struct Values {
+    static constexpr int kWords = N * (int)sizeof(T) / 4, PW = 4 / (int)sizeof(T);
     static constexpr uint32_t kAbs = sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
     uint32_t w[kWords];
-    __device__ __forceinline__ void load_fast(const T* p) {
+    __device__ __forceinline__ void load16(const T* p) {  // 16-byte aligned
 #pragma unroll
         for (int q = 0; q < kWords; q += 4) {
             const uint4 u = reinterpret_cast<const uint4*>(p)[q / 4];
             w[q] = u.x; w[q + 1] = u.y; w[q + 2] = u.z; w[q + 3] = u.w;
         }
     }
-    __device__ __forceinline__ void load(const T* p, int left, int width) {
+    __device__ __forceinline__ void load32(const T* p) {  // 32-byte aligned
+#pragma unroll
+        for (int q = 0; q < kWords; q += 8)
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(w[q]), "=r"(w[q + 1]), "=r"(w[q + 2]), "=r"(w[q + 3]), "=r"(w[q + 4]), "=r"(w[q + 5]),
+                           "=r"(w[q + 6]), "=r"(w[q + 7])
+                         : "l"(p + q * PW));
+    }
+    __device__ __forceinline__ void load(const T* p, int left, int width) {  // N = 8
         float v[8];
         load8(p, left, width, v);
 #pragma unroll
@@ -298,14 +306,15 @@ struct Eight {
     }
     __device__ __forceinline__ void drop_infinities() {
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+        for (int t = 0; t < N; ++t)
             w[t / PW] = with_part<T>(w[t / PW], t % PW, finite_or_nan(part_of<T>(w[t / PW], t % PW)));
     }
-    __device__ __forceinline__ uint2 encode(float inverse) const {
-        float v[8];
+    // the codes of values 4 q .. 4 q + 3
+    __device__ __forceinline__ uint32_t encode(int q, float inverse) const {
+        float v[4];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) v[t] = part_of<T>(w[t / PW], t % PW);
-        return make_uint2(encode4(v, inverse), encode4(v + 4, inverse));
+        for (int t = 0; t < 4; ++t) v[t] = part_of<T>(w[(4 * q + t) / PW], (4 * q + t) % PW);
+        return encode4(v, inverse);
     }
 };
 
@@ -326,13 +335,13 @@ __global__ void __launch_bounds__(256)
     const int groups = (int)(nb.div + 3) / 4;
     for (uint32_t f0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kPairsPerWarp; f0 < total; f0 += stride) {
         const Pairs at(f0 + half, nb);
-        Eight<T> v[kSteps];
+        Values<T, 8> v[kSteps];
         int to[kSteps];
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
             const int col = at.b[s] * kBlock + col8;
             if (FAST)
-                v[s].load_fast(X + (int64_t)min(at.row[s], n - 1) * ldx + min(col, d - 8));
+                v[s].load16(X + (int64_t)min(at.row[s], n - 1) * ldx + min(col, d - 8));
             else
                 v[s].load(X + (int64_t)at.row[s] * ldx + col, at.row[s] < n ? d - col : 0, width);
         }
@@ -359,11 +368,76 @@ __global__ void __launch_bounds__(256)
             const int e = block_exponent(half ? hi : lo);
             const float inverse = __uint_as_float((uint32_t)(127 - e) << 23);
             if (to[s] >= 0 && col < pitch)
-                *reinterpret_cast<uint2*>(codes + (int64_t)to[s] * pitch + col) = v[s].encode(inverse);
+                *reinterpret_cast<uint2*>(codes + (int64_t)to[s] * pitch + col) =
+                    make_uint2(v[s].encode(0, inverse), v[s].encode(1, inverse));
             if ((lane & 15) == s) {
                 mine = e + 127;
                 my_to = to[s];
                 my_b = at.b[s];
+            }
+        }
+        if (my_to >= 0) scales[scale_at(my_to, my_b, groups)] = (uint8_t)mine;
+    }
+}
+
+// The same where d is a multiple of 16 and the rows of X are 32-byte aligned: 16 values
+// per lane, 8 lanes per pair, two steps of four pairs in flight. With 8 values per lane
+// the work to find them kept 16-bit inputs from the memory's rate (65,536 x 768 bf16
+// 29 us).
+template <class T, bool SLOTS>
+__global__ void __launch_bounds__(256)
+    k_block8_write_wide(const T* __restrict__ X, int n, int d, int64_t ldx, const int64_t* __restrict__ slots, int first,
+                        const int* __restrict__ claims, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                        int64_t rows, FastDiv nb, int* status) {
+    pdl_wait();
+    pdl_release();
+    constexpr int kWideSteps = 2;
+    static_assert(4 * kWideSteps == kPairsPerWarp, "the launch shape of k_block8_write");
+    const int lane = threadIdx.x & 31, part = lane >> 3, col16 = (lane & 7) * 16;
+    const uint32_t total = (uint32_t)n * nb.div;
+    const uint32_t stride = gridDim.x * (blockDim.x >> 5) * kPairsPerWarp;
+    const int groups = (int)(nb.div + 3) / 4;
+    for (uint32_t f0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kPairsPerWarp; f0 < total; f0 += stride) {
+        Values<T, 16> v[kWideSteps];
+        int row[kWideSteps], b[kWideSteps], to[kWideSteps];
+#pragma unroll
+        for (int s = 0; s < kWideSteps; ++s) {  // (lanes past the data load a place inside it and drop it)
+            const uint32_t f = f0 + 4 * s + part;
+            row[s] = (int)nb.quotient(f);
+            b[s] = (int)(f - (uint32_t)row[s] * nb.div);
+            v[s].load32(X + (int64_t)min(row[s], n - 1) * ldx + min(b[s] * kBlock + col16, d - 16));
+        }
+#pragma unroll
+        for (int s = 0; s < kWideSteps; ++s) {
+            to[s] = -1;
+            if (row[s] < n) to[s] = SLOTS ? (int)slot_of(slots, 0, row[s], rows, status) : first + row[s];
+        }
+        int mine = 0, my_to = -1, my_b = 0;  // lane 8 part + s keeps the exponent of step s
+#pragma unroll
+        for (int s = 0; s < kWideSteps; ++s) {
+            const int col = b[s] * kBlock + col16;
+            if (SLOTS && !last_of_slot(slots, claims, row[s], n, to[s], lane & 7, 8)) to[s] = -1;
+            if (col >= d) v[s].clear();
+            uint32_t a = v[s].largest();
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+            if (__any_sync(0xFFFFFFFFu, a >= 0x7F800000u)) {  // (as in k_block8_write)
+                v[s].drop_infinities();
+                a = v[s].largest();
+                if (a >= 0x7F800000u) a = 0u;  // NaN alone
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+            }
+            const int e = block_exponent(a);
+            const float inverse = __uint_as_float((uint32_t)(127 - e) << 23);
+            if (to[s] >= 0 && col < d)
+                *reinterpret_cast<uint4*>(codes + (int64_t)to[s] * d + col) =
+                    make_uint4(v[s].encode(0, inverse), v[s].encode(1, inverse), v[s].encode(2, inverse),
+                               v[s].encode(3, inverse));
+            if ((lane & 7) == s) {
+                mine = e + 127;
+                my_to = to[s];
+                my_b = b[s];
             }
         }
         if (my_to >= 0) scales[scale_at(my_to, my_b, groups)] = (uint8_t)mine;
