@@ -460,10 +460,13 @@ struct ColTile {
     static constexpr int kRows = 8 * V;
     static constexpr int kPerWord = 4 / (int)sizeof(T);
     static constexpr uint32_t kAbs = sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+    // (4,096 rows of 16,384 values: fp32 with 6 blocks on an SM 51.6 us, with 5 54.3; bf16
+    // with 5 38.0, with 6, on 40 registers, 40.3)
+    static constexpr int kBlocksPerSm = sizeof(T) == 4 ? 6 : 5;
 };
 
 template <class T>
-__global__ void __launch_bounds__(256, 5)
+__global__ void __launch_bounds__(256, ColTile<T>::kBlocksPerSm)
     k_block8_write_cols(const T* __restrict__ X, int n, int d, int64_t ldx, int width,
                         const int64_t* __restrict__ slots, int64_t first, const int* __restrict__ claims,
                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t rows, int pitch,
