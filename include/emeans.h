@@ -431,8 +431,8 @@ int em_block8_layout(int64_t rows, int64_t d, int64_t* pitch, int64_t* code_byte
  * slot the last stays. Rows that the call does not name are left as they are. Value j
  * of row i is X[i * row_stride + j * col_stride] (strides in elements): one of the two
  * is 1, so a matrix and the transpose of one are both taken as they lie (row_stride 0
- * repeats one row); 16-byte aligned rows load fastest. n x ceil(d / 128) < 2^31, here
- * and in em_block8_read. */
+ * repeats one row); rows that start on 32 bytes, with d a multiple of 16, load fastest.
+ * n x ceil(d / 128) is at most 2^31 - 2^16, here and in em_block8_read. */
 int em_block8_write(const em_block8_t* m, const void* X, int dtype, int64_t n, int64_t row_stride, int64_t col_stride,
                     int64_t first, const int64_t* slots, void* stream);
 
@@ -456,7 +456,8 @@ int em_block8_matmul(const em_block8_t* a, int64_t na, const em_block8_t* b, int
                      int64_t row_stride, void* stream);
 
 /* Waits for `stream` and reports a device-side error raised in the matrix's status
- * word since the last check (EM_E_BOUNDS, EM_E_TIMEOUT), which it clears. */
+ * word since the last check (EM_E_BOUNDS, EM_E_TIMEOUT), which it clears. EM_E_STATE
+ * while the stream is being captured. */
 int em_block8_check(const em_block8_t* m, void* stream);
 
 /* ---- data parallelism (README "Several GPUs": DistributedEmeans) ----

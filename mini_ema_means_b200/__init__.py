@@ -280,10 +280,10 @@ class Block8:
 
     The memory is torch tensors: `codes` (rows x pitch, uint8), `scales` (uint8, in the
     order of the header), `claims` and `status` (scratch). `codes` and `scales` may be
-    given, filled or not; otherwise they are made and stand for zeros. The calls run on
-    `stream` (a torch.cuda.Stream; by default the current stream of the matrix's device)
-    and do not wait for it. A Block8 is also an X for Model.train, begin, lloyd, assign
-    and mse."""
+    given, filled or not; otherwise they are made, on the current stream, and stand for
+    zeros. The calls run on `stream` (a torch.cuda.Stream; by default the current stream
+    of the matrix's device) and do not wait for it. A Block8 is also an X for
+    Model.train, begin, lloyd, assign and mse."""
 
     def __init__(self, rows, d, device=None, codes=None, scales=None):
         import torch

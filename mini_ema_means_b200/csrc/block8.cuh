@@ -2,6 +2,16 @@
 // checks, launch shapes and the C ABI. Included at the end of emeans.cu.
 #pragma once
 
+// CK that also takes the error off the runtime's record, so that no later call finds it.
+#define B8_CK(call)                                                                                \
+    do {                                                                                           \
+        const cudaError_t e_ = (call);                                                             \
+        if (e_ != cudaSuccess) {                                                                   \
+            cudaGetLastError();                                                                    \
+            return fail(EM_E_CUDA, "%s: %s", #call, cudaGetErrorString(e_));                       \
+        }                                                                                          \
+    } while (0)
+
 namespace {
 
 // Makes a device current for a call and puts the caller's back.
@@ -45,6 +55,9 @@ int same_device(const char* what, const void* const* ptrs, int count, int* dev) 
 }
 
 constexpr int64_t kB8MaxD = 1ll << 24;
+// The kernels count the (row, block) pairs of a call in 31 bits, and look a few past the
+// last (2^31 pairs of whole blocks are 270 GB of codes).
+constexpr int64_t kB8MaxPairs = (1ll << 31) - (1ll << 16);
 
 int64_t b8_pitch(int64_t d) { return (d + 15) / 16 * 16; }
 int64_t b8_blocks(int64_t d) { return (d + b8::kBlock - 1) / b8::kBlock; }
@@ -79,9 +92,8 @@ int b8_check_dtype(int dtype, const void* p, const char* what) {
 
 // Rows [first, first + n) or slots; n within the limits of the row indexes.
 int b8_check_rows(const em_block8_t* m, int64_t first, const int64_t* slots, int64_t n) {
-    // (the kernels count (row, block) pairs in 31 bits; 2^31 pairs are 270 GB of codes)
-    if (n < 0 || n >= (1ll << 31) || n * b8_blocks(m->d) >= (1ll << 31))
-        return fail(EM_E_INVAL, "need 0 <= n and n x ceil(d / 128) < 2^31 (n = %lld)", (long long)n);
+    if (n < 0 || n > kB8MaxPairs || n * b8_blocks(m->d) > kB8MaxPairs)
+        return fail(EM_E_INVAL, "need 0 <= n and n x ceil(d / 128) <= 2^31 - 2^16 (n = %lld)", (long long)n);
     if (slots) {
         if (first != 0) return fail(EM_E_INVAL, "first must be 0 with slots");
         if ((uintptr_t)slots & 7) return fail(EM_E_INVAL, "slots must be 8-byte aligned");
@@ -115,12 +127,14 @@ int b8_device(int dev, DeviceFacts* out) {
         cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
         if (major != 10 || minor != 0) return fail(EM_E_NODEVICE, "this library is built for sm_100a (B200)");
-        CK(cudaDeviceGetAttribute(&f.sms, cudaDevAttrMultiProcessorCount, dev));
-        CK(cudaDeviceGetAttribute(&f.clock_khz, cudaDevAttrClockRate, dev));
+        B8_CK(cudaDeviceGetAttribute(&f.sms, cudaDevAttrMultiProcessorCount, dev));
+        B8_CK(cudaDeviceGetAttribute(&f.clock_khz, cudaDevAttrClockRate, dev));
         if (!b8_smem_attribute(b8::k_block8_matmul<128, 4, false>, b8::MmCfg<128, false>::kSmem) ||
             !b8_smem_attribute(b8::k_block8_matmul<128, 2, false>, b8::MmCfg<128, false>::kSmem) ||
             !b8_smem_attribute(b8::k_block8_matmul<128, 4, true>, b8::MmCfg<128, true>::kSmem) ||
             !b8_smem_attribute(b8::k_block8_matmul<128, 2, true>, b8::MmCfg<128, true>::kSmem) ||
+            !b8_smem_attribute(b8::k_block8_matmul<32, 4, false>, b8::MmCfg<32, false>::kSmem) ||
+            !b8_smem_attribute(b8::k_block8_matmul<32, 2, false>, b8::MmCfg<32, false>::kSmem) ||
             !b8_smem_attribute(b8::k_block8_matmul<32, 4, true>, b8::MmCfg<32, true>::kSmem) ||
             !b8_smem_attribute(b8::k_block8_matmul<32, 2, true>, b8::MmCfg<32, true>::kSmem) ||
             !b8_smem_attribute(b8::k_block8_matmul_pair<4, false>, b8::kSmem2) ||
@@ -154,7 +168,7 @@ int b8_write(bool cols, const void* X_, int64_t n, int64_t ldx, const int64_t* s
     const int d = (int)m->d, pitch = (int)b8_pitch(m->d);
     if (!cols) {
         if (d % 16 == 0 && (uintptr_t)X % 32 == 0 && ldx * sizeof(T) % 32 == 0) {
-            CK(launch_k(true, slots ? b8::k_block8_write_wide<T, true> : b8::k_block8_write_wide<T, false>,
+            B8_CK(launch_k(true, slots ? b8::k_block8_write_wide<T, true> : b8::k_block8_write_wide<T, false>,
                         dim3(b8_pair_grid(n, nb, sms)), dim3(256), 0, st, X, (int)n, d, ldx, slots, (int)first, claims,
                         codes, scales, m->rows, b8::FastDiv((uint32_t)nb), m->status));
             return EM_OK;
@@ -163,13 +177,13 @@ int b8_write(bool cols, const void* X_, int64_t n, int64_t ldx, const int64_t* s
         const bool fast = width * sizeof(T) == 16 && d % 8 == 0;
         auto* kernel = slots ? (fast ? b8::k_block8_write<T, true, true> : b8::k_block8_write<T, true, false>)
                              : (fast ? b8::k_block8_write<T, false, true> : b8::k_block8_write<T, false, false>);
-        CK(launch_k(true, kernel, dim3(b8_pair_grid(n, nb, sms)), dim3(256), 0, st, X, (int)n, d, ldx, width, slots,
+        B8_CK(launch_k(true, kernel, dim3(b8_pair_grid(n, nb, sms)), dim3(256), 0, st, X, (int)n, d, ldx, width, slots,
                     (int)first, claims, codes, scales, m->rows, pitch, b8::FastDiv((uint32_t)nb), m->status));
         return EM_OK;
     }
     const int64_t row_tiles = (n + b8::ColTile<T>::kRows - 1) / b8::ColTile<T>::kRows;
     const int grid = (int)std::min<int64_t>(row_tiles * nb, (int64_t)sms * kB8PerSm);
-    CK(launch_k(true, b8::k_block8_write_cols<T>, dim3(grid), dim3(256), 0, st, X, (int)n, d, ldx,
+    B8_CK(launch_k(true, b8::k_block8_write_cols<T>, dim3(grid), dim3(256), 0, st, X, (int)n, d, ldx,
                 b8::vector_width<T>(X, ldx), slots, first, claims, codes, scales, m->rows, pitch, b8::FastDiv((uint32_t)row_tiles), m->status));
     return EM_OK;
 }
@@ -182,12 +196,12 @@ int b8_read_as(const em_block8_t* m, int64_t first, const int64_t* slots, int64_
     const auto codes = static_cast<const uint8_t*>(m->codes), scales = static_cast<const uint8_t*>(m->scales);
     T* rows_out = static_cast<T*>(out);
     if (columns == m->d && m->d % 16 == 0 && (uintptr_t)out % 32 == 0 && ldo * sizeof(T) % 32 == 0) {
-        CK(launch_k(true, slots ? b8::k_block8_read_wide<T, true> : b8::k_block8_read_wide<T, false>, grid, dim3(256), 0,
+        B8_CK(launch_k(true, slots ? b8::k_block8_read_wide<T, true> : b8::k_block8_read_wide<T, false>, grid, dim3(256), 0,
                     st, codes, scales, m->rows, (int)m->d, slots, (int)first, (int)n, rows_out, ldo,
                     b8::FastDiv((uint32_t)nb), m->status));
         return EM_OK;
     }
-    CK(launch_k(true, slots ? b8::k_block8_read<T, true> : b8::k_block8_read<T, false>, grid, dim3(256), 0, st, codes,
+    B8_CK(launch_k(true, slots ? b8::k_block8_read<T, true> : b8::k_block8_read<T, false>, grid, dim3(256), 0, st, codes,
                 scales, m->rows, (int)b8_pitch(m->d), (int)m->d, slots, (int)first, (int)n, rows_out, ldo, (int)columns,
                 b8::vector_width<T>(out, ldo), b8::FastDiv((uint32_t)nb), m->status));
     return EM_OK;
@@ -211,6 +225,7 @@ static int read_block8(em_model* m, const em_block8_t* x, int64_t n, __nv_bfloat
     if (x->d != m->d || n > x->rows)
         return fail(EM_E_INVAL, "the block8 matrix is %lld x %lld: the model needs %lld rows of %lld values",
                     (long long)x->rows, (long long)x->d, (long long)n, (long long)m->d);
+    CKR(b8_check_rows(x, 0, nullptr, n));
     const void* ptrs[] = {x->codes, x->scales, x->status};
     int dev;
     CKR(same_device("a block8 input", ptrs, 3, &dev));
@@ -252,7 +267,7 @@ template <int BN, bool SWAP>
 int b8_launch_single(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmSA, const CUtensorMap& tmSB,
                      const b8::MmArgs& p, size_t esz, int sms, cudaStream_t st) {
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
-    CK(launch_k(true, esz == 4 ? b8::k_block8_matmul<BN, 4, SWAP> : b8::k_block8_matmul<BN, 2, SWAP>,
+    B8_CK(launch_k(true, esz == 4 ? b8::k_block8_matmul<BN, 4, SWAP> : b8::k_block8_matmul<BN, 2, SWAP>,
                 dim3((unsigned)std::min<int64_t>(tiles, sms)), dim3(b8::kMmThreads), b8::MmCfg<BN, SWAP>::kSmem, st, tmA,
                 tmB, tmSA, tmSB, p));
     return EM_OK;
@@ -267,8 +282,8 @@ int b8_launch_matmul(const em_block8_t* a, int64_t na, const em_block8_t* b, int
     const int64_t t1 = ((na + 127) / 128) * ((nb + 127) / 128);
     const int64_t t2 = ((na + 255) / 256) * ((nb + b8::kPairN - 1) / b8::kPairN);
     const int64_t pairs = std::max(sms / 2, 1);
-    const bool pair = !swap && t1 > sms && (t2 + pairs - 1) / pairs * 384 <= (t1 + sms - 1) / sms * 400;
-    const bool narrow = swap && nb <= 32;
+    const bool narrow = nb <= 32;
+    const bool pair = !swap && !narrow && t1 > sms && (t2 + pairs - 1) / pairs * 384 <= (t1 + sms - 1) / sms * 400;
     const int box_b = pair ? b8::kPairN / 2 : narrow ? 32 : 128;
     CUtensorMap tmA, tmB, tmSA, tmSB;
     CKR(make_tmap8(&tmA, a->codes, a->rows, (int)a->d, (int)b8_pitch(a->d), 128));
@@ -293,13 +308,15 @@ int b8_launch_matmul(const em_block8_t* a, int64_t na, const em_block8_t* b, int
         const bool ast = p.nkb <= b8::kAstBlocks && 2 * p.nkb >= 3 * (int)esz;
         auto* kernel = esz == 4 ? (ast ? b8::k_block8_matmul_pair<4, true> : b8::k_block8_matmul_pair<4, false>)
                                 : (ast ? b8::k_block8_matmul_pair<2, true> : b8::k_block8_matmul_pair<2, false>);
-        CK(launch_k(true, kernel, dim3((unsigned)(2 * std::min(t2, pairs))), dim3(b8::kPairThreads),
+        B8_CK(launch_k(true, kernel, dim3((unsigned)(2 * std::min(t2, pairs))), dim3(b8::kPairThreads),
                     ast ? b8::kSmem2Ast : b8::kSmem2, st, tmA, tmB, tmSA, tmSB, tmOut, p));
         return EM_OK;
     }
     p.m_tiles = (int)((na + 127) / 128);
     p.n_tiles = (int)((nb + box_b - 1) / box_b);
-    if (narrow) return b8_launch_single<32, true>(tmA, tmB, tmSA, tmSB, p, esz, sms, st);
+    if (narrow)
+        return swap ? b8_launch_single<32, true>(tmA, tmB, tmSA, tmSB, p, esz, sms, st)
+                    : b8_launch_single<32, false>(tmA, tmB, tmSA, tmSB, p, esz, sms, st);
     if (swap) return b8_launch_single<128, true>(tmA, tmB, tmSA, tmSB, p, esz, sms, st);
     return b8_launch_single<128, false>(tmA, tmB, tmSA, tmSB, p, esz, sms, st);
 }
@@ -331,13 +348,13 @@ int em_block8_write(const em_block8_t* m, const void* X, int dtype, int64_t n, i
     int dev;
     CKR(same_device("em_block8_write", ptrs, 6, &dev));
     DeviceGuard guard;
-    CK(guard.to(dev));
+    B8_CK(guard.to(dev));
     DeviceFacts f;
     CKR(b8_device(dev, &f));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int* claims = nullptr;
     if (slots && n > b8::kScanRows) {
-        CK(launch_k(true, b8::k_block8_claim, dim3(grid_for(n, 256, f.sms)), dim3(256), 0, st, slots, n, m->rows,
+        B8_CK(launch_k(true, b8::k_block8_claim, dim3(grid_for(n, 256, f.sms)), dim3(256), 0, st, slots, n, m->rows,
                     m->claims));
         claims = m->claims;
     }
@@ -362,7 +379,7 @@ int em_block8_read(const em_block8_t* m, int64_t first, const int64_t* slots, in
     int dev;
     CKR(same_device("em_block8_read", ptrs, 5, &dev));
     DeviceGuard guard;
-    CK(guard.to(dev));
+    B8_CK(guard.to(dev));
     DeviceFacts f;
     CKR(b8_device(dev, &f));
     return b8_read(m, first, slots, n, out, dtype, row_stride, m->d, f.sms, static_cast<cudaStream_t>(stream));
@@ -384,7 +401,7 @@ int em_block8_matmul(const em_block8_t* a, int64_t na, const em_block8_t* b, int
     int dev;
     CKR(same_device("em_block8_matmul", ptrs, 6, &dev));
     DeviceGuard guard;
-    CK(guard.to(dev));
+    B8_CK(guard.to(dev));
     DeviceFacts f;
     CKR(b8_device(dev, &f));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -407,14 +424,18 @@ int em_block8_check(const em_block8_t* m, void* stream) {
     int dev;
     CKR(same_device("em_block8_check", ptrs, 1, &dev));
     DeviceGuard guard;
-    CK(guard.to(dev));
+    B8_CK(guard.to(dev));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+    B8_CK(cudaStreamIsCapturing(st, &capturing));
+    if (capturing != cudaStreamCaptureStatusNone)
+        return fail(EM_E_STATE, "em_block8_check waits for the stream: not while it is captured");
     int32_t h = 0;
-    CK(cudaMemcpyAsync(&h, m->status, sizeof(h), cudaMemcpyDeviceToHost, st));
-    CK(cudaStreamSynchronize(st));
+    B8_CK(cudaMemcpyAsync(&h, m->status, sizeof(h), cudaMemcpyDeviceToHost, st));
+    B8_CK(cudaStreamSynchronize(st));
     if (h != 0) {
-        CK(cudaMemsetAsync(m->status, 0, sizeof(h), st));
-        CK(cudaStreamSynchronize(st));
+        B8_CK(cudaMemsetAsync(m->status, 0, sizeof(h), st));
+        B8_CK(cudaStreamSynchronize(st));
         return fail(h, h == EM_E_TIMEOUT ? "a device-side wait exceeded its limit"
                                          : "a slot is outside the matrix (device error %d)",
                     (int)h);

@@ -973,21 +973,23 @@ __device__ __forceinline__ void store_rows(const uint32_t (&sum)[NS][32], uint8_
 //
 // SWAP: the M operand is the one whose rows are the output's columns (few output
 // rows): a lane holds one output column and a warp stores 32 neighbours at once.
-// With few rows the product streams the long operand once, and what counts is bytes in
-// flight: BN = 32 keeps the stages small and lets two groups of four epilogue warps
-// take tiles in turn, four accumulators ahead.
+// With few rows on one side the product streams the long operand once, and what counts
+// is bytes in flight: BN = 32 keeps the stages small and lets two groups of four
+// epilogue warps take tiles in turn, four accumulators ahead (300,000 rows of 128 with
+// 24 others: 15 us where they are the columns of the result; where they are its rows 28,
+// and 66 in 256 x 192 tiles).
 //
 // The blocks of all of a CTA's tiles form one sequence, PER of them to a stage: a
 // barrier round trip serves PER blocks whatever the rows' length.
 
 template <int BN, bool SWAP>
 struct MmCfg {
-    static constexpr int kPer = SWAP ? 2 : 1;
-    static constexpr int kStages = !SWAP ? 5 : BN == 32 ? 5 : 3;
+    static constexpr int kPer = SWAP || BN == 32 ? 2 : 1;
+    static constexpr int kStages = BN == 32 ? (SWAP ? 5 : 4) : (SWAP ? 3 : 5);
     static constexpr int kBTile = BN * 128;
     static constexpr int kCodes = kCodeTile + kBTile;  // codes of one block
     static constexpr int kSf = 2 * kAtomBytes;
-    static constexpr bool kTurns = SWAP && BN == 32;   // the epilogue's halves take tiles in turn
+    static constexpr bool kTurns = BN == 32;           // the epilogue's halves take tiles in turn
     static constexpr int kAcc = kTurns ? 4 : 2;
     static constexpr int kSmem = 1024 + 256 + (SWAP ? 0 : kTurnBytes) + kStages * kPer * (kCodes + kSf);
     static constexpr int kSfCols = 8;

@@ -260,7 +260,8 @@ def test_product(em, na, nb, d, kind):
 
 # More than a wave of 128 x 128 tiles: pairs of CTAs. Rows of 3 to 6 blocks (A kept),
 # more and fewer, ragged in both directions, one span and several.
-LARGE = [(2500, 1500, 300), (1500, 3001, 700), (20000, 777, 96), (2100, 2000, 1300), (1300, 2050, 2100), (1921, 1729, 640)]
+LARGE = [(2500, 1500, 300), (1500, 3001, 700), (20000, 777, 96), (2100, 2000, 1300), (1300, 2050, 2100), (1921, 1729, 640),
+         (3000, 1, 900), (4000, 32, 128), (3777, 24, 70), (2500, 33, 260)]
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
@@ -461,6 +462,23 @@ def test_a_captured_run_is_replayed_on_new_inputs(em):
         every = torch.empty(rows, d, device="cuda")
         store.read(every)
         _assert_product(scores, B.held(_f64(qs)), _f64(every), "f32")
+
+
+def test_check_is_refused_while_the_stream_is_captured(em):
+    m = em.Block8(10, 20)
+    x = torch.ones(10, 20, device="cuda")
+    m.write(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.write(x)
+        with pytest.raises(em.EmeansError) as e:
+            m.check()
+        m.write(x)
+    assert e.value.code == em.EM_E_STATE
+    graph.replay()
+    m.check()
+    _check_rows(m, np.arange(10), x)
 
 
 def test_two_streams_at_once(em):
