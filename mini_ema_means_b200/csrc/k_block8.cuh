@@ -853,6 +853,7 @@ struct MmArgs {
     int64_t m_rows, n_rows;  // rows of the M and N operands that the product takes
     int nkb;                 // blocks along the rows
     int m_tiles, n_tiles;
+    int split;               // CTAs (a cluster) that share a tile, one span each; 1: none do
     int bf16;                // 16-bit results: bf16 rather than fp16
     int vec_ok;              // 16-byte aligned output rows
     long long wait_limit;
@@ -981,6 +982,10 @@ __device__ __forceinline__ void store_rows(const uint32_t (&sum)[NS][32], uint8_
 //
 // The blocks of all of a CTA's tiles form one sequence, PER of them to a stage: a
 // barrier round trip serves PER blocks whatever the rows' length.
+//
+// Long rows with few tiles: a cluster of `split` CTAs shares a tile, one span of the
+// rows each. The spans' results meet in shared memory, and the cluster's first CTA adds
+// them in order: the sums are those of a CTA that does all spans, bit for bit.
 
 template <int BN, bool SWAP>
 struct MmCfg {
@@ -1024,6 +1029,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const long long drain_limit = p.wait_limit > 4000000000ll ? p.wait_limit : 4000000000ll;
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
     const int groups = (p.nkb + 3) / 4;
+    // this CTA's tiles and the blocks of their rows that it takes
+    const bool shared_tile = p.split > 1;
+    const int rank = shared_tile ? (int)(blockIdx.x % p.split) : 0;
+    const int64_t first = shared_tile ? blockIdx.x / p.split : blockIdx.x, step = shared_tile ? tiles : gridDim.x;
+    const int kb_lo = rank * kSpan, kb_hi = shared_tile ? min(p.nkb, kb_lo + kSpan) : p.nkb;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -1057,9 +1067,9 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         int stage = 0, part = 0;  // the next block's stage, and its place there
         uint32_t phase = 0, armed = 0, armed_parity = 0;
         bool ok = true;
-        for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int64_t t = first; t < tiles && ok; t += step) {
             const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
-            for (int kb = 0; kb < p.nkb; ++kb) {
+            for (int kb = kb_lo; kb < kb_hi; ++kb) {
                 if (part == 0) {
                     ok = wait_warp(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag);
                     if (!ok) break;
@@ -1102,17 +1112,17 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         bool ok = true;
         const uint64_t desc0 = smem_desc(0u, 2ull, 1024u);
         const uint32_t a_base = smem_u32(sA) >> 4, b_base = smem_u32(sB) >> 4;
-        for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int64_t t = first; t < tiles && ok; t += step) {
             // four blocks share a group of exponents; unrolled, so that what the MMAs take
             // but a block's stage is fixed
-            for (int kb0 = 0; kb0 < p.nkb && ok; kb0 += 4) {
+            for (int kb0 = kb_lo; kb0 < kb_hi && ok; kb0 += 4) {
                 if (kb0 % kSpan == 0)
                     ok = wait_warp(smem_u32(&tempty[acc]), acc_phase ^ 1u, p.wait_limit, p.status, abort_flag);
                 if (++slot == C::kSfSlots) slot = 0;
                 const uint32_t sf = tmem_base + (uint32_t)(C::kSfBase + slot * C::kSfCols);
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-                const int blocks = min(4, p.nkb - kb0);
-                const bool last = kb0 % kSpan + 4 == kSpan || kb0 + blocks == p.nkb;
+                const int blocks = min(4, kb_hi - kb0);
+                const bool last = kb0 % kSpan + 4 == kSpan || kb0 + blocks == kb_hi;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (i >= blocks) break;
@@ -1154,21 +1164,46 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             umma_commit(smem_u32(drain));
             mbar_drain(smem_u32(drain), 0u, drain_limit);
         }
-    } else {
-        const int ew = warp - 3;
-        const int q = warp & 3, half = ew >> 2;
+    }
+    // ---------------- epilogue
+    const int ew = warp - 3;
+    const int q = warp & 3, half = ew >> 2;
+    constexpr int kCols = C::kTurns ? BN : BN / 2;  // columns a warp takes
+    constexpr int NS = kCols / 32;
+    auto store = [&](const uint32_t (&sum)[NS][32], int64_t row0, int64_t col0) {
+        if (SWAP) {
+            const int64_t j = row0 + lane;  // output column
+            const int rows = (int)min(p.n_rows - col0, (int64_t)kCols);
+            uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + (col0 * p.ldo + j) * OB;
+            if (j < p.m_rows) {
+#pragma unroll
+                for (int i = 0; i < NS; ++i)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        if (32 * i + e < rows) {
+                            if (OB == 4)
+                                *reinterpret_cast<uint32_t*>(dst) = sum[i][e];
+                            else
+                                *reinterpret_cast<uint16_t*>(dst) = (uint16_t)pack_out(sum[i][e], 0u, p.bf16);
+                        }
+                        dst += p.ldo * OB;
+                    }
+            }
+        } else {
+            store_rows<OB, NS>(sum, turn + ew * 32 * 128, lane, row0, col0, p);
+        }
+    };
+    // a shared tile's results of this CTA's span: [warp][column][lane], over the ring
+    // (which is done with by the time the accumulator is complete)
+    float* part = reinterpret_cast<float*>(sA) + ew * NS * 32 * 32 + lane;
+    static_assert(8 * NS * 32 * 32 * 4 <= S * PER * kCodeTile, "the ring holds a tile's results");
+    if (warp >= 3) {
         const uint32_t lane_base = (uint32_t)(32 * q) << 16;
-        constexpr int kCols = C::kTurns ? BN : BN / 2;  // columns a warp takes
-        constexpr int NS = kCols / 32;
-        uint8_t* buf = turn + ew * 32 * 128;
-        const int spans = (p.nkb + kSpan - 1) / kSpan;
+        const int spans = shared_tile ? 1 : (p.nkb + kSpan - 1) / kSpan;
         int64_t span = C::kTurns ? (int64_t)half * spans : 0;  // spans of the CTA before this tile's
         bool ok = true;
-        for (int64_t t = blockIdx.x + (C::kTurns ? (int64_t)half * gridDim.x : 0); t < tiles && ok;
-             t += (C::kTurns ? 2 : 1) * (int64_t)gridDim.x) {
+        for (int64_t t = first + (C::kTurns ? half * step : 0); t < tiles && ok; t += (C::kTurns ? 2 : 1) * step) {
             const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
-            const int64_t row0 = (int64_t)m * 128 + 32 * q;
-            const int64_t col0 = (int64_t)n * BN + (C::kTurns ? 0 : half * kCols);
             uint32_t sum[NS][32];
             clear_sums(sum);
             for (int s = 0; s < spans; ++s) {
@@ -1188,28 +1223,39 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             }
             if (C::kTurns) span += spans;  // the other half's tile
             if (!ok) break;
-            if (SWAP) {
-                const int64_t j = row0 + lane;  // output column
-                const int rows = (int)min(p.n_rows - col0, (int64_t)kCols);
-                uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + (col0 * p.ldo + j) * OB;
-                if (j < p.m_rows) {
+            if (shared_tile) {
 #pragma unroll
-                    for (int i = 0; i < NS; ++i)
+                for (int i = 0; i < NS; ++i)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            if (32 * i + e < rows) {
-                                if (OB == 4)
-                                    *reinterpret_cast<uint32_t*>(dst) = sum[i][e];
-                                else
-                                    *reinterpret_cast<uint16_t*>(dst) = (uint16_t)pack_out(sum[i][e], 0u, p.bf16);
-                            }
-                            dst += p.ldo * OB;
-                        }
-                }
+                    for (int e = 0; e < 32; ++e) part[(32 * i + e) * 32] = __uint_as_float(sum[i][e]);
             } else {
-                store_rows<OB, NS>(sum, buf, lane, row0, col0, p);
+                store(sum, (int64_t)m * 128 + 32 * q, (int64_t)n * BN + (C::kTurns ? 0 : half * kCols));
             }
         }
+    }
+    if (shared_tile) {
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+        if (rank == 0 && warp >= 3 && (!C::kTurns || half == 0)) {
+            uint32_t sum[NS][32];
+            clear_sums(sum);
+            for (int r = 0; r < p.split; ++r) {
+                uint32_t from;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(smem_u32(part)), "r"(r));
+#pragma unroll
+                for (int i = 0; i < NS; ++i)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float v;
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from + (32 * i + e) * 128) : "memory");
+                        sum[i][e] = __float_as_uint(__uint_as_float(sum[i][e]) + v);
+                    }
+            }
+            const int m = (int)(first / p.n_tiles), n = (int)(first - (int64_t)m * p.n_tiles);
+            store(sum, (int64_t)m * 128 + 32 * q, (int64_t)n * BN + (C::kTurns ? 0 : half * kCols));
+        }
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
     }
 
     tc_fence_before();

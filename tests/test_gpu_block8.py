@@ -236,7 +236,8 @@ def _plain(n, d, seed):
 
 SHAPES = [(1, 1, 1), (1, 1, 4096), (1, 300, 768), (3, 129, 128), (16, 1000, 96), (33, 40, 33), (128, 129, 640),
           (129, 128, 130), (127, 1, 700), (200, 16, 513), (300, 257, 512), (513, 770, 200), (260, 300, 1100),
-          (1000, 1, 64), (2, 5, 9000), (150, 140, 5000)]
+          (1000, 1, 64), (2, 5, 9000), (150, 140, 5000), (40, 300, 2049),
+          (17, 500, 8192), (300, 20, 3000), (140, 129, 1025)]
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
@@ -282,20 +283,21 @@ def test_large_product(em, na, nb, d, kind):
         assert (wide[0] == 5).all() and (wide[na + 1] == 5).all() and (wide[:, nb:] == 5).all()
 
 
-def test_one_row_of_results_is_the_same_whoever_computes_it(em):
-    """Few rows, some and many take different kernels; the sums of a result are the
-    same in each, bit for bit."""
-    d = 900
+@pytest.mark.parametrize("d", [900, 1100, 5000, 8192])
+def test_one_row_of_results_is_the_same_whoever_computes_it(em, d):
+    """Few rows, some and many take different kernels, long rows with few tiles several
+    CTAs to a tile; the sums of a result are the same in each, bit for bit."""
     x, y = _plain(2000, d, 1), _plain(1700, d, 2)
     A, Bm = em.Block8(2000, d), em.Block8(1700, d)
     A.write(x.cuda())
     Bm.write(y.cuda())
     all_rows = torch.empty(2000, 1700, device="cuda")
     A.matmul(Bm, all_rows)
-    for n in (1, 20, 32, 33, 128, 129, 300):
-        out = torch.empty(n, 1700, device="cuda")
+    for n, k in ((1, 1700), (20, 300), (32, 1700), (33, 90), (128, 1700), (129, 130), (300, 257), (300, 1700), (200, 3)):
+        out = torch.empty(n, k, device="cuda")
         A.matmul(Bm, out)
-        assert torch.equal(out, all_rows[:n]), n
+        assert torch.equal(out, all_rows[:n, :k]), (n, k)
+    A.check()
 
 
 def test_product_of_a_matrix_with_itself_and_repeats(em):
