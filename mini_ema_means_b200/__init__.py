@@ -282,8 +282,9 @@ class Block8:
     order of the header), `claims` and `status` (scratch). `codes` and `scales` may be
     given, filled or not; otherwise they are made, on the current stream, and stand for
     zeros. The calls run on `stream` (a torch.cuda.Stream; by default the current stream
-    of the matrix's device) and do not wait for it. A Block8 is also an X for
-    Model.train, begin, lloyd, assign and mse."""
+    of the matrix's device; one given by its handle alone is not recorded with the
+    memory it uses) and do not wait for it. A Block8 is also an X for Model.train, begin,
+    lloyd, assign and mse, which wait for the current stream of its device first."""
 
     def __init__(self, rows, d, device=None, codes=None, scales=None):
         import torch
@@ -321,10 +322,17 @@ class Block8:
     def shape(self):
         return (self.rows, self.d)
 
-    def _stream(self, stream):
+    def _stream(self, stream, *used):
+        """The handle to launch on. A given torch stream is recorded with the memory used,
+        so that the caching allocator keeps it until that stream is done."""
         if stream is None:
             return self._current(self._index)
-        return stream if isinstance(stream, int) else stream.cuda_stream
+        if isinstance(stream, int):
+            return stream
+        for t in (self.codes, self.scales, self.claims, self.status, *used):
+            if t is not None:
+                t.record_stream(stream)
+        return stream.cuda_stream
 
     def _here(self, t, name):
         if t.get_device() != self._index or (self._index < 0 and t.device != self.device):
@@ -364,7 +372,7 @@ class Block8:
         or into rows slots[i] (-1: not written; the last of equal slots stays)."""
         n, dtype, rs, cs = self._matrix(X, self.d, "X")
         rc = em_block8_write(self._ref, X.data_ptr(), dtype, n, rs, cs, first, self._slots(slots, n, first),
-                             self._stream(stream))
+                             self._stream(stream, X, slots))
         if rc:
             check(rc, "em_block8_write")
 
@@ -374,7 +382,7 @@ class Block8:
         if cs != 1 and n:
             raise ValueError("the rows of out must be contiguous")
         rc = em_block8_read(self._ref, first, self._slots(slots, n, first), n, out.data_ptr(), dtype,
-                            rs if n > 1 else self.d, self._stream(stream))
+                            rs if n > 1 else self.d, self._stream(stream, out, slots))
         if rc:
             check(rc, "em_block8_read")
         return out
@@ -388,7 +396,7 @@ class Block8:
         if cs != 1 and na and nb:
             raise ValueError("the rows of out must be contiguous")
         rc = em_block8_matmul(self._ref, na, other._ref, nb, out.data_ptr(), dtype, rs if na > 1 else nb,
-                              self._stream(stream))
+                              self._stream(stream, out, other.codes, other.scales))
         if rc:
             check(rc, "em_block8_matmul")
         return out
@@ -444,6 +452,8 @@ class Model:
             value = {"throughput": 0, "quality": 1, "auto": 2}[value]
         if name == "input_dtype" and not isinstance(value, (int, float)):
             value = 1 if "bfloat16" in str(value) or str(value) == "bf16" else 3 if str(value) == "block8" else 0
+        if name == "input_dtype":
+            self._raw_dtype = None
         check(em_set_option(self.h, self._OPTS[name], float(value)), f"em_set_option({name})")
 
     def get_option(self, name) -> float:
@@ -454,9 +464,12 @@ class Model:
     def _dtype_of(self, X):
         was = int(self.get_option("input_dtype"))
         if isinstance(X, Block8):
-            if was != EM_DTYPE_BLOCK8:
-                self._raw_dtype = was  # what a raw pointer points to
+            import torch
+
+            raw = was if was != EM_DTYPE_BLOCK8 else self._raw_dtype  # what a raw pointer points to
             self.set_option("input_dtype", EM_DTYPE_BLOCK8)
+            self._raw_dtype = raw
+            torch.cuda.current_stream(X.device).synchronize()  # (the model reads on a stream of its own)
         elif hasattr(X, "dtype"):
             self.set_option("input_dtype", 1 if "bfloat16" in str(X.dtype) else 0)
         elif was == EM_DTYPE_BLOCK8 and self._raw_dtype is not None:

@@ -602,6 +602,49 @@ def test_a_model_takes_a_block8_matrix(em):
     m.close()
 
 
+def test_a_model_waits_for_the_writes_of_the_current_stream(em):
+    """A matrix written on the current stream, behind a long queue, and handed to a model
+    at once; then what set_option says of raw pointers."""
+    n, d, k = 200_000, 256, 8
+    x = _plain(n, d, 7).cuda()
+    m8, ref = em.Block8(n, d), em.Block8(n, d)
+    ref.write(x)
+    m = em.Model(d, k, seed=2)
+    m.train(ref, epochs=0.05)
+    want = m.mse(ref)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(200):
+            m8.write(x * -1.0)
+        m8.write(x)
+        assert m.mse(m8) == want
+    m.set_option("input_dtype", "block8")
+    assert m.mse(int(__import__("ctypes").addressof(m8.view)), n=n) == want
+    with pytest.raises(em.EmeansError):
+        m.set_option("input_dtype", 2)
+    m.close()
+
+
+def test_memory_dropped_after_a_call_on_another_stream(em):
+    """Inputs freed by the caller while a call on a given stream is still queued are not
+    handed out again before it is done."""
+    st = torch.cuda.Stream()
+    m = em.Block8(4096, 512)
+    x = _plain(4096, 512, 3)
+    xg = x.cuda()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(50_000_000)
+    m.write(xg, stream=st)
+    del xg
+    for _ in range(4):
+        torch.full((4096, 512), 9.0, device="cuda")
+    st.synchronize()
+    _check_rows(m, np.arange(0, 4096, 97), x[::97])
+
+
 def test_the_operators_together(em):
     """As a service uses them: a store filled in pieces, centroids trained on it, and
     queries scored against the nearest cluster's stored rows, gathered by number."""
