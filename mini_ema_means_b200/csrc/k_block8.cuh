@@ -632,7 +632,9 @@ __global__ void __launch_bounds__(256, 5)
 
 // The same where d is a multiple of 16 and the output's rows are 32-byte aligned: 16
 // values per lane, 8 lanes per pair, two steps of four pairs in flight, and 32-byte
-// stores. A lane's work to find its values is shared by twice as many.
+// stores. A lane's work to find its values is shared by twice as many. 32 registers, so
+// that an SM is full of warps (65,536 rows of 768 gathered to bf16: 27.2 us, with 40 of
+// its 64 warps 30.0).
 __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                  "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -640,7 +642,7 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
 }
 
 template <class T, bool SLOTS>
-__global__ void __launch_bounds__(256, 5)
+__global__ void __launch_bounds__(256, 8)
     k_block8_read_wide(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int d,
                        const int64_t* __restrict__ slots, int first, int n, T* __restrict__ out, int64_t ldo, FastDiv nb,
                        int* status) {
