@@ -446,8 +446,7 @@ int em_block8_read(const em_block8_t* m, int64_t first, const int64_t* slots, in
 
 /* out[i * row_stride + j] = sum over t of a[i][t] * b[j][t] for rows [0, na) of a and
  * [0, nb) of b, which have the same d: products of the held values, exact, summed in
- * fp32 on the tensor cores and rounded once to dtype (sums below fp32's normal numbers
- * may come out as zero). `out` overlaps neither matrix.
+ * fp32 on the tensor cores and rounded once to dtype. `out` overlaps neither matrix.
  * The result for a row holding NaN is NaN and no other row's is touched. Device-side
  * errors are raised in a's status word.
  * Gradients of out = A B^T for dOut (na x nb) are two more such products: dA = dOut B

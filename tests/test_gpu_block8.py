@@ -351,6 +351,17 @@ def test_scales_of_every_block_enter(em):
     _assert_product(out, B.held(_f64(x)), B.held(_f64(y)), "f32")
 
 
+def test_scales_at_the_ends_of_the_range(em):
+    """Sums of 128 equal powers of two are exact: subnormal results, scales that cancel,
+    and results beyond fp32."""
+    m, out = em.Block8(2, 128), torch.empty(2, 2, device="cuda")
+    for p, q in ((-70, -70), (-126, -10), (-64, -62), (100, -100), (119, -126), (60, 59), (100, 100)):
+        m.write(torch.tensor([[2.0 ** p], [2.0 ** q]], device="cuda").expand(2, 128).contiguous())
+        m.matmul(m, out)
+        want = torch.tensor([[2.0 * p + 7, p + q + 7.0], [p + q + 7.0, 2.0 * q + 7]], dtype=torch.float64).exp2().float()
+        assert torch.equal(out.cpu(), want), (p, q, out, want)
+
+
 # ---------------------------------------------------------------- gradients
 
 
