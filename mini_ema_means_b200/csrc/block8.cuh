@@ -201,9 +201,16 @@ int b8_read_as(const em_block8_t* m, int64_t first, const int64_t* slots, int64_
                     b8::FastDiv((uint32_t)nb), m->status));
         return EM_OK;
     }
+    const int width = b8::vector_width<T>(out, ldo);
+    if (width == 1) {
+        B8_CK(launch_k(true, slots ? b8::k_block8_read_any<T, true> : b8::k_block8_read_any<T, false>, grid, dim3(256), 0,
+                       st, codes, scales, m->rows, (int)b8_pitch(m->d), (int)m->d, slots, (int)first, (int)n, rows_out,
+                       ldo, (int)columns, b8::FastDiv((uint32_t)nb), m->status));
+        return EM_OK;
+    }
     B8_CK(launch_k(true, slots ? b8::k_block8_read<T, true> : b8::k_block8_read<T, false>, grid, dim3(256), 0, st, codes,
-                scales, m->rows, (int)b8_pitch(m->d), (int)m->d, slots, (int)first, (int)n, rows_out, ldo, (int)columns,
-                b8::vector_width<T>(out, ldo), b8::FastDiv((uint32_t)nb), m->status));
+                   scales, m->rows, (int)b8_pitch(m->d), (int)m->d, slots, (int)first, (int)n, rows_out, ldo, (int)columns,
+                   width, b8::FastDiv((uint32_t)nb), m->status));
     return EM_OK;
 }
 
