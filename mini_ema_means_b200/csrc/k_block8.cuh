@@ -92,29 +92,6 @@ __host__ __device__ __forceinline__ int vector_width(const void* base, int64_t l
 }
 
 template <class T, int W>
-__device__ __forceinline__ void load8_as(const T* p, float v[8]) {
-#pragma unroll
-    for (int q = 0; q < 8 / W; ++q) {
-        const Vec<T, W> x = reinterpret_cast<const Vec<T, W>*>(p)[q];
-#pragma unroll
-        for (int t = 0; t < W; ++t) v[q * W + t] = to_f32(x.v[t]);
-    }
-}
-
-// 8 values from p, of which `left` exist (zeros after them).
-template <class T>
-__device__ __forceinline__ void load8(const T* p, int left, int width, float v[8]) {
-    if (left >= 8 && width == 16 / (int)sizeof(T)) {
-        load8_as<T, 16 / sizeof(T)>(p, v);
-    } else if (left >= 8 && width > 1) {
-        load8_as<T, 8 / sizeof(T)>(p, v);
-    } else {
-#pragma unroll
-        for (int t = 0; t < 8; ++t) v[t] = t < left ? to_f32(p[t]) : 0.0f;
-    }
-}
-
-template <class T, int W>
 __device__ __forceinline__ void store8_as(T* p, const float v[8]) {
 #pragma unroll
     for (int q = 0; q < 8 / W; ++q) {
@@ -286,11 +263,35 @@ struct Values {
                            "=r"(w[q + 6]), "=r"(w[q + 7])
                          : "l"(p + q * PW));
     }
-    __device__ __forceinline__ void load(const T* p, int left, int width) {  // N = 8
-        float v[8];
-        load8(p, left, width, v);
+    // 8-byte aligned, `left` values exist (zeros after them): the whole pieces of 8 bytes
+    // first, for all steps, with no branch between them, then a last broken one
+    static constexpr int kPiece = 8 / (int)sizeof(T);
+    __device__ __forceinline__ void load_pieces(const T* p, int left) {
 #pragma unroll
-        for (int t = 0; t < 8; ++t) w[t / PW] = with_part<T>(t % PW ? w[t / PW] : 0u, t % PW, v[t]);
+        for (int q = 0; q < kWords / 2; ++q) {
+            const uint2 u = (q + 1) * kPiece <= left ? reinterpret_cast<const uint2*>(p)[q] : make_uint2(0u, 0u);
+            w[2 * q] = u.x;
+            w[2 * q + 1] = u.y;
+        }
+    }
+    __device__ __forceinline__ void load_rest(const T* p, int left) {
+        if (left <= 0 || left >= N || left % kPiece == 0) return;
+#pragma unroll
+        for (int t = 0; t < N; ++t)
+            if (t >= left / kPiece * kPiece && t < left) w[t / PW] = with_part<T>(w[t / PW], t % PW, to_f32(p[t]));
+    }
+    // any alignment, one by one
+    __device__ __forceinline__ void load_single(const T* p, int left) {
+#pragma unroll
+        for (int q = 0; q < kWords; ++q) {
+            if (PW == 1) {
+                w[q] = q < left ? reinterpret_cast<const uint32_t*>(p)[q] : 0u;
+            } else {
+                const uint16_t lo = 2 * q < left ? reinterpret_cast<const uint16_t*>(p)[2 * q] : (uint16_t)0;
+                const uint16_t hi = 2 * q + 1 < left ? reinterpret_cast<const uint16_t*>(p)[2 * q + 1] : (uint16_t)0;
+                w[q] = (uint32_t)lo | (uint32_t)hi << 16;
+            }
+        }
     }
     __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -337,13 +338,28 @@ __global__ void __launch_bounds__(256)
         const Pairs at(f0 + half, nb);
         Values<T, 8> v[kSteps];
         int to[kSteps];
+        if (FAST) {
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int col = at.b[s] * kBlock + col8;
-            if (FAST)
-                v[s].load16(X + (int64_t)min(at.row[s], n - 1) * ldx + min(col, d - 8));
-            else
-                v[s].load(X + (int64_t)at.row[s] * ldx + col, at.row[s] < n ? d - col : 0, width);
+            for (int s = 0; s < kSteps; ++s)
+                v[s].load16(X + (int64_t)min(at.row[s], n - 1) * ldx + min(at.b[s] * kBlock + col8, d - 8));
+        } else {
+            const T* src[kSteps];
+            int left[kSteps];
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const int col = at.b[s] * kBlock + col8;
+                src[s] = X + (int64_t)at.row[s] * ldx + col;
+                left[s] = at.row[s] < n ? d - col : 0;
+            }
+            if (width > 1) {
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) v[s].load_pieces(src[s], left[s]);
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) v[s].load_rest(src[s], left[s]);
+            } else {
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) v[s].load_single(src[s], left[s]);
+            }
         }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
