@@ -226,8 +226,8 @@ int b8_read(const em_block8_t* m, int64_t first, const int64_t* slots, int64_t n
 
 }  // namespace
 
-// The rows [0, n) of a block8 matrix as a model's bf16 data (pitch m->ld, zeros past d).
-static int read_block8(em_model* m, const em_block8_t* x, int64_t n, __nv_bfloat16* out) {
+// Whether the rows [0, n) of a block8 matrix can be a model's data.
+static int check_block8(const em_model* m, const em_block8_t* x, int64_t n) {
     CKR(b8_check(x));
     if (x->d != m->d || n > x->rows)
         return fail(EM_E_INVAL, "the block8 matrix is %lld x %lld: the model needs %lld rows of %lld values",
@@ -237,6 +237,11 @@ static int read_block8(em_model* m, const em_block8_t* x, int64_t n, __nv_bfloat
     int dev;
     CKR(same_device("a block8 input", ptrs, 3, &dev));
     if (dev != m->dev) return fail(EM_E_INVAL, "the block8 matrix is on device %d, the model on %d", dev, m->dev);
+    return EM_OK;
+}
+
+// The rows [0, n) of a block8 matrix as a model's bf16 data (pitch m->ld, zeros past d).
+static int read_block8(em_model* m, const em_block8_t* x, int64_t n, __nv_bfloat16* out) {
     return b8_read(x, 0, nullptr, n, out, EM_DTYPE_BF16, m->ld, m->ld, m->sms, m->stream);
 }
 

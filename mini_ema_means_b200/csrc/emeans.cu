@@ -491,7 +491,13 @@ static int grid_for(int64_t work, int block, int sms, int per_sm = 8) {
     return (int)std::max<int64_t>(g, 1);
 }
 
+static int check_block8(const em_model* m, const em_block8_t* x, int64_t n);
 static int read_block8(em_model* m, const em_block8_t* x, int64_t n, __nv_bfloat16* out);
+
+// What can be refused of X before a call allocates or changes anything.
+static int check_input(const em_model* m, const void* X, int64_t n) {
+    return m->in_dtype == EM_DTYPE_BLOCK8 ? check_block8(m, static_cast<const em_block8_t*>(X), n) : EM_OK;
+}
 
 // EM_OPT_CHECK_FINITE: EM_E_NONFINITE if any of `count` values is NaN or infinite.
 static int check_finite(em_model* m, const void* src, int64_t count, bool bf16) {
@@ -505,8 +511,8 @@ static int check_finite(em_model* m, const void* src, int64_t count, bool bf16) 
     return EM_OK;
 }
 
-// Makes a bf16 n x ld device copy of X (or uses X in place). *out receives the
-// row source the kernels read.
+// Makes a bf16 n x ld device copy of X (or uses X in place), which check_input has
+// passed. *out receives the row source the kernels read.
 static int prepare_input(em_model* m, const void* X, int64_t n, DBuf<__nv_bfloat16>& own,
                          const __nv_bfloat16** out) {
     if (!X || n < 1) return fail(EM_E_INVAL, "X is NULL or n < 1");
@@ -1660,6 +1666,7 @@ int em_begin(em_model* m, const void* X, int64_t n, double epochs) {
     if (n >= (1ll << 31)) return fail(EM_E_INVAL, "n must be below 2^31");
     if (!(epochs > 0.0)) return fail(EM_E_INVAL, "epochs must be positive");
     CKR(set_device(m));
+    CKR(check_input(m, X, n));
     // a data-parallel run: n is this rank's share, the recipe is the whole job's
     const int64_t W = m->dp_world, n_total = n * W;
     if (n_total >= (1ll << 31)) return fail(EM_E_INVAL, "the rows of all ranks must be below 2^31");
@@ -1778,6 +1785,7 @@ int em_lloyd(em_model* m, const void* X, int64_t n, int64_t iters) {
     if (!m) return fail(EM_E_INVAL, "model is NULL");
     if (n < m->k || n >= (1ll << 31) || iters < 0) return fail(EM_E_INVAL, "bad Lloyd arguments");
     CKR(set_device(m));
+    CKR(check_input(m, X, n));
     CKR(drop_prefetch(m));
     m->running = false;
     m->n_local = n;
@@ -1866,6 +1874,7 @@ int em_assign(em_model* m, const void* X, int64_t n, int64_t* labels, float* dis
     if (!m) return fail(EM_E_INVAL, "model is NULL");
     if (n < 1 || n >= (1ll << 31)) return fail(EM_E_INVAL, "need 1 <= n < 2^31");
     CKR(set_device(m));
+    CKR(check_input(m, X, n));
     const bool lab_dev = labels && is_device_ptr(labels);
     const bool dist_dev = dists && is_device_ptr(dists);
     int64_t* lab_p = nullptr;
@@ -1908,6 +1917,7 @@ int em_mse(em_model* m, const void* X, int64_t n, double* out) {
     if (!m || !out) return fail(EM_E_INVAL, "NULL argument");
     if (n < 1 || n >= (1ll << 31)) return fail(EM_E_INVAL, "need 1 <= n < 2^31");
     CKR(set_device(m));
+    CKR(check_input(m, X, n));
     DBuf<__nv_bfloat16> tmp;
     int rc = assign_pass(m, X, n, nullptr, nullptr, m->scalar.p, tmp);
     double s = 0.0;
