@@ -391,6 +391,7 @@ struct em_model {
     DBuf<unsigned long long> keys;
     DBuf<double> block_err, part, step_err, scalar;
     DBuf<int64_t> labels_last, labels64;
+    int64_t labels_n = 0;  // rows of the run that labels_last is of
     // revival scratch
     DBuf<int32_t> rv_dead, rv_donor, rv_order, rv_times, rv_ndead;
     DBuf<double> rv_tree, rv_target;
@@ -1670,19 +1671,25 @@ int em_begin(em_model* m, const void* X, int64_t n, double epochs) {
     // a data-parallel run: n is this rank's share, the recipe is the whole job's
     const int64_t W = m->dp_world, n_total = n * W;
     if (n_total >= (1ll << 31)) return fail(EM_E_INVAL, "the rows of all ranks must be below 2^31");
-    CKR(compute_recipe(n_total, m->k, m->d, epochs, effective_law(m), m->opt_batch, m->opt_alpha0, &m->rec));
-    if (m->rec.batch_size > n_total) return fail(EM_E_INVAL, "batch size larger than n");
+    em_recipe_t rec{};
+    CKR(compute_recipe(n_total, m->k, m->d, epochs, effective_law(m), m->opt_batch, m->opt_alpha0, &rec));
+    if (rec.batch_size > n_total) return fail(EM_E_INVAL, "batch size larger than n");
     if (W > 1) {
-        CKR(check_dp_recipe(m->rec, W));
+        CKR(check_dp_recipe(rec, W));
         if (m->revival == EM_REVIVE_RESAMPLE)
             return fail(EM_E_INVAL, "resampling draws rows of the whole batch; use it with one rank");
     }
     m->running = false;
-    m->n = n_total;
-    m->n_local = n;
     const int sp = span_begin(m, EM_PHASE_PREPARE);
     CKR(prepare_input(m, X, n, m->Xown, &m->X));
     CKR(prepare_fp8(m, m->X, n));
+    // the data are accepted: what the model reports is this run's from here on
+    m->have_run = false;
+    m->rec = rec;
+    m->n = n_total;
+    m->n_local = n;
+    m->labels_n = 0;
+    m->last_rows = 0;
     const int64_t b = m->rec.batch_size / W;  // this rank's rows of a full batch
     CKR(drop_prefetch(m));
     CK(cudaStreamSynchronize(m->stream));  // no gather of a previous run still writes the slots
@@ -1715,6 +1722,7 @@ int em_begin(em_model* m, const void* X, int64_t n, double epochs) {
     if (m->capture) {
         CKR(m->labels_last.ensure(n));
         CK(cudaMemsetAsync(m->labels_last.p, 0xFF, n * sizeof(int64_t), m->stream));
+        m->labels_n = n;
     }
     if (m->comm) CKR(m->stats.ensure((size_t)m->k * m->ld + m->k + 1));
     CKR(start_centroids(m));
@@ -1788,9 +1796,10 @@ int em_lloyd(em_model* m, const void* X, int64_t n, int64_t iters) {
     CKR(check_input(m, X, n));
     CKR(drop_prefetch(m));
     m->running = false;
+    CKR(prepare_input(m, X, n, m->Xown, &m->X));
+    m->have_run = false;
     m->n_local = n;
     m->n = n * m->dp_world;  // data-parallel: every rank's rows, one summed update per iteration
-    CKR(prepare_input(m, X, n, m->Xown, &m->X));
     CKR(prepare_fp8(m, m->X, n));
     CKR(ensure_batch_buffers(m, n));
     if (m->comm) CKR(m->stats.ensure((size_t)m->k * m->ld + m->k + 1));
@@ -1825,7 +1834,6 @@ int em_lloyd(em_model* m, const void* X, int64_t n, int64_t iters) {
         CKR(launch_settle(m, m->X, m->xn.p, m->labels.p, nullptr, m->dists.p, true, nullptr, nullptr, 0));
         CKR(launch_reduce(m, m->X, n, nbl, 1.0, 0, m->scalar.p));
     }
-    m->have_run = false;
     m->last_was_lloyd = 1;
     return check_device_errors(m);
 }
@@ -1943,9 +1951,9 @@ int em_centroids(const em_model* m, float* out) {
 
 int em_labels(const em_model* m, int64_t* out) {
     if (!m || !out) return fail(EM_E_INVAL, "NULL argument");
-    if (!m->capture || !m->labels_last.p || m->last_was_lloyd) return fail(EM_E_STATE, "no captured labels");
+    if (!m->capture || m->labels_n < 1 || m->last_was_lloyd) return fail(EM_E_STATE, "no captured labels");
     CKR(set_device(m));
-    CK(cudaMemcpyAsync(out, m->labels_last.p, m->n_local * sizeof(int64_t), cudaMemcpyDefault, m->stream));
+    CK(cudaMemcpyAsync(out, m->labels_last.p, m->labels_n * sizeof(int64_t), cudaMemcpyDefault, m->stream));
     CK(cudaStreamSynchronize(m->stream));
     return EM_OK;
 }

@@ -85,3 +85,47 @@ def test_a_refused_matrix_leaves_the_run_as_it_was(em):
         got.append((_centroids(m), lab, torch.from_numpy(m.obj())))
         m.close()
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def _finished(em):
+    """A finished run on N rows that checks its data, and what it reports."""
+    m = em.Model(D, K, seed=5, check_finite=1)
+    m.train(_store(em), epochs=2.0)
+    lab = torch.full((2 * N,), -7, dtype=torch.int64)
+    m.labels(lab)
+    return m, (lab, m.recipe(), m.obj().tolist(), m.stats()["steps_done"])
+
+
+@pytest.mark.parametrize("kind", ["block8", "float32", "bfloat16"])
+def test_data_that_are_not_finite_leave_the_last_run_readable(em, kind):
+    """More rows than the last run had, one of them NaN: em_begin, em_train and em_lloyd
+    refuse them, and the last run's labels, recipe and error history stay, with its number
+    of rows; then the same model trains as a new one does."""
+    x = torch.randn(2 * N - 1, D, generator=torch.Generator().manual_seed(1))
+    good = x.cuda()
+    x[N + 7, 3] = float("nan")
+    X = x.cuda()
+    if kind == "block8":
+        X = em.Block8(2 * N - 1, D)
+        X.write(x.cuda())
+        X.check()
+    elif kind == "bfloat16":
+        X = X.bfloat16()
+    m, want = _finished(em)
+    for call in (lambda: m.begin(X), lambda: m.train(X), lambda: m.lloyd(X, 2)):
+        with pytest.raises(em.EmeansError) as e:
+            call()
+        assert e.value.code == em.EM_E_NONFINITE
+        lab = torch.full((2 * N,), -7, dtype=torch.int64)
+        m.labels(lab)
+        assert torch.equal(lab, want[0]) and (lab[N:] == -7).all()
+        assert (m.recipe(), m.obj().tolist(), m.stats()["steps_done"]) == want[1:]
+        with pytest.raises(em.EmeansError) as e:
+            m.step(1)
+        assert e.value.code == em.EM_E_STATE
+    fresh = em.Model(D, K, seed=5)
+    for t in (m, fresh):
+        t.train(good, epochs=1.0)
+    assert torch.equal(_centroids(m), _centroids(fresh))
+    m.close()
+    fresh.close()
