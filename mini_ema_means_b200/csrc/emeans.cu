@@ -1104,7 +1104,7 @@ static int launch_step(em_model* m, const StepPlan& p) {
     }
     sp = span_begin(m, EM_PHASE_UPDATE);
     const int nbl = (int)((rows + 255) / 256);
-    const int capture = (m->capture && p.last_pass) ? 1 : 0;
+    const int capture = (m->capture && m->labels_n > 0 && p.last_pass) ? 1 : 0;
     launch_k(m->pdl, k_labels, nbl, 256, 0, m->stream, m->keys.p, m->last_split, m->fp8 ? b.xn8.p : b.xn.p, (int)rows,
                                          (int)m->k, b.X.p, m->ld, m->cq.p, b.ids.p, m->labels.p, m->dists.p,
                                          m->cnt.p, m->rank.p, m->block_err.p, m->labels_last.p, capture,
@@ -1155,7 +1155,7 @@ static std::vector<uint64_t> graph_signature(const em_model* m) {
     const int64_t ints[] = {m->n, m->d, m->k, m->ld, m->kc, m->R, m->sms, m->rec.batch_size, m->rec.total_steps,
                             m->rec.passes, m->rec.rows_last_pass, (int64_t)m->seed, m->revival, m->finalize,
                             m->capture, m->auto_revive, m->assign_kernel, m->wait_cycles, m->exact_ties,
-                            m->spherical, m->prefetch, m->n_local, m->dp_world, m->dp_rank,
+                            m->spherical, m->prefetch, m->n_local, m->labels_n, m->dp_world, m->dp_rank,
                             (int64_t)(uintptr_t)m->comm, (int64_t)(uintptr_t)m->stats.p, m->fp8,
                             (int64_t)(uintptr_t)m->slot[0].X8.p, (int64_t)(uintptr_t)m->slot[1].X8.p,
                             (int64_t)(uintptr_t)m->cq8.p, (int64_t)(uintptr_t)m->fp8_shift.p,

@@ -129,3 +129,23 @@ def test_data_that_are_not_finite_leave_the_last_run_readable(em, kind):
     assert torch.equal(_centroids(m), _centroids(fresh))
     m.close()
     fresh.close()
+
+
+def test_labels_kept_from_the_middle_of_a_run_on_are_refused(em):
+    """A run begun without keeping labels has none, also where the option is set later."""
+    m = em.Model(D, K, seed=5)
+    m.train(_store(em, n=500), epochs=1.0)
+    m.set_option("capture_labels", 0)
+    store = _store(em)
+    m.begin(store, epochs=2.0)
+    m.set_option("capture_labels", 1)
+    m.step(10 ** 6)
+    m.finalize()
+    with pytest.raises(em.EmeansError) as e:
+        m.labels(torch.empty(N, dtype=torch.int64))
+    assert e.value.code == em.EM_E_STATE
+    m.train(store, epochs=2.0)
+    lab = torch.empty(N, dtype=torch.int64)
+    m.labels(lab)
+    assert (lab >= 0).all() and (lab < K).all()
+    m.close()
