@@ -283,7 +283,10 @@ class Block8:
     given, filled or not; otherwise they are made, on the current stream, and stand for
     zeros. The calls run on `stream` (a torch.cuda.Stream; by default the current stream
     of the matrix's device; one given by its handle alone is not recorded with the
-    memory it uses) and do not wait for it. A Block8 is also an X for Model.train, begin,
+    memory it uses) and do not wait for it. They are no part of autograd: write takes
+    the values of X as if detached, and what the calls write counts as modified in place
+    (`out`, `codes`, `scales`), so that a backward pass which saved it refuses. An `out`
+    that requires gradients is refused, but under torch.no_grad(). A Block8 is also an X for Model.train, begin,
     lloyd, assign and mse, which wait for the current stream of its device first."""
 
     def __init__(self, rows, d, device=None, codes=None, scales=None):
@@ -313,6 +316,10 @@ class Block8:
         self._index = -1 if self.device.index is None else self.device.index
         self._types = {torch.float32: EM_DTYPE_F32, torch.bfloat16: EM_DTYPE_BF16, torch.float16: EM_DTYPE_F16}
         self._int64 = torch.int64
+        self._held = (self.codes, self.scales)
+        # marks tensors as modified in place (the public function wraps this one, for 0.1 us)
+        self._modified = getattr(torch._C, "_increment_version", None) or torch.autograd.graph.increment_version
+        self._grad_mode = torch.is_grad_enabled
         # the current stream's handle alone (torch.cuda.current_stream makes an object of
         # it, 2 us of a call of 7)
         self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -346,7 +353,8 @@ class Block8:
         shape = t.shape
         if len(shape) != 2 or shape[1] != cols:
             raise ValueError(f"{name} must be 2-D with {cols} columns, not {tuple(shape)}")
-        self._here(t, name)
+        if t.get_device() != self._index or self._index < 0:
+            self._here(t, name)
         rs, cs = t.stride()
         # a dimension of one element has no stride of its own
         if cols == 1:
@@ -362,7 +370,8 @@ class Block8:
             raise ValueError("slots must be a contiguous 1-D int64 tensor")
         if len(slots) != n:
             raise ValueError(f"{len(slots)} slots for {n} rows")
-        self._here(slots, "slots")
+        if slots.get_device() != self._index or self._index < 0:
+            self._here(slots, "slots")
         if first:
             raise ValueError("first must be 0 with slots")
         return slots.data_ptr() if n else None
@@ -375,22 +384,28 @@ class Block8:
                              self._stream(stream, X, slots))
         if rc:
             check(rc, "em_block8_write")
+        self._modified(self._held)
 
     def read(self, out, first=0, slots=None, stream=None):
         """Reads out.shape[0] rows from `first` on, or rows slots[i] (-1: zeros), into out."""
         n, dtype, rs, cs = self._matrix(out, self.d, "out")
+        if out.requires_grad and self._grad_mode():
+            raise ValueError("out requires gradients, which this call has none of")
         if cs != 1 and n:
             raise ValueError("the rows of out must be contiguous")
         rc = em_block8_read(self._ref, first, self._slots(slots, n, first), n, out.data_ptr(), dtype,
                             rs if n > 1 else self.d, self._stream(stream, out, slots))
         if rc:
             check(rc, "em_block8_read")
+        self._modified((out,))
         return out
 
     def matmul(self, other, out, stream=None):
         """out[i, j] = row i of this matrix . row j of `other`, for out's shape."""
         nb = out.shape[-1]
         na, dtype, rs, cs = self._matrix(out, nb, "out")
+        if out.requires_grad and self._grad_mode():
+            raise ValueError("out requires gradients, which this call has none of")
         if other.device != self.device:
             raise ValueError(f"the other matrix is on {other.device}, this one on {self.device}")
         if cs != 1 and na and nb:
@@ -399,6 +414,7 @@ class Block8:
                               self._stream(stream, out, other.codes, other.scales))
         if rc:
             check(rc, "em_block8_matmul")
+        self._modified((out,))
         return out
 
     def check(self, stream=None):
