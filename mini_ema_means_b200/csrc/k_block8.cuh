@@ -21,6 +21,7 @@
 
 #include "k_assign.cuh"
 #include "k_data.cuh"
+#include "ring.cuh"
 
 namespace em {
 namespace b8 {
@@ -941,6 +942,21 @@ struct MmArgs {
     int* status;
 };
 
+// At least about 2 s, whatever limit the waits had.
+__device__ __forceinline__ long long drain_limit(const MmArgs& p) { return max(p.wait_limit, 4000000000ll); }
+
+// The end of a CTA that gave up: its shared and tensor memory go to the next one, so that
+// every load of the ring must have landed, whichever role gave up and wherever the loaders
+// stood. `begun`: fills of the loader that is ahead. A fill that another loader did not
+// begin never completes; `limit` cycles, for all fills together, end the wait for it, a
+// million times what a load takes.
+template <int S>
+__device__ __forceinline__ void drain_ring(const uint64_t* full, uint32_t begun, long long limit) {
+    const long long t0 = clock64();
+    for (uint32_t i = ring_first(begun, S); i != begun; ++i)
+        tc::mbar_drain(tc::smem_u32(&full[ring_stage(i, S)]), ring_parity(i, S), max(limit - (clock64() - t0), 0ll));
+}
+
 __device__ __forceinline__ uint32_t pack_out(uint32_t lo, uint32_t hi, int bf16) {
     uint32_t r;
     if (bf16) {
@@ -1105,9 +1121,9 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     uint64_t* drain = tempty + ACC;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    uint32_t* begun_by = tmem_slot + 2;  // stages that each loader began
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long drain_limit = p.wait_limit > 4000000000ll ? p.wait_limit : 4000000000ll;
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
     const int groups = (p.nkb + 3) / 4;
     // this CTA's tiles and the blocks of their rows that it takes
@@ -1146,7 +1162,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     if (warp == 0 || warp == 2) {
         const bool loads_a = warp == 0;
         int stage = 0, part = 0;  // the next block's stage, and its place there
-        uint32_t phase = 0, armed = 0, armed_parity = 0;
+        uint32_t phase = 0, begun = 0;
         bool ok = true;
         for (int64_t t = first; t < tiles && ok; t += step) {
             const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
@@ -1154,8 +1170,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 if (part == 0) {
                     ok = wait_warp(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag);
                     if (!ok) break;
-                    armed |= 1u << stage;
-                    armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                    ++begun;
                 }
                 if (elect_one()) {
                     const uint32_t fb = smem_u32(&full[stage]);
@@ -1184,9 +1199,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         if (part > 0 && elect_one())  // the last stage's missing blocks
             for (; part < PER; ++part) mbar_arrive(smem_u32(&full[stage]));
         __syncwarp();
-        if (!ok && lane == 0 && loads_a)
-            for (int s = 0; s < S; ++s)
-                if (armed & (1u << s)) mbar_drain(smem_u32(&full[s]), (armed_parity >> s) & 1u, drain_limit);
+        if (lane == 0) begun_by[loads_a ? 0 : 1] = begun;
     } else if (warp == 1) {
         int stage = 0, part = 0, acc = 0, slot = C::kSfSlots - 1;
         uint32_t phase = 0, acc_phase = 0;
@@ -1240,10 +1253,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     acc_phase ^= 1u;
                 }
             }
-        }
-        if (!ok && elect_one()) {
-            umma_commit(smem_u32(drain));
-            mbar_drain(smem_u32(drain), 0u, drain_limit);
         }
     }
     // ---------------- epilogue
@@ -1341,6 +1350,13 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag) {  // a role gave up: loads and MMAs may be in flight
+        if (threadIdx.x == 0) drain_ring<S>(full, max(begun_by[0], begun_by[1]), drain_limit(p));
+        if (warp == 1 && elect_one()) {
+            umma_commit(smem_u32(drain));
+            mbar_drain(smem_u32(drain), 0u, drain_limit(p));
+        }
+    }
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
@@ -1396,6 +1412,14 @@ __device__ __forceinline__ uint32_t in_even_cta(uint32_t addr) {
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
     return r;
 }
+
+// A word written to the place of `p` in CTA `cta` of the pair.
+__device__ __forceinline__ void store_cta(const volatile void* p, uint32_t cta, uint32_t value) {
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(const_cast<const void*>(p))), "r"(cta));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(value) : "memory");
+}
+__device__ __forceinline__ void store_even(const uint32_t* p, uint32_t value) { store_cta(p, 0u, value); }
 
 // A load into this CTA's shared memory that completes on a barrier of the pair's even CTA.
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
@@ -1466,11 +1490,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     uint64_t* aempty = tfull + 8;     // (AST; each CTA) the MMAs are done with them
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 9);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* other_abort = abort_flag + 1;  // the other CTA's, as it ended
+    uint32_t* begun_by = tmem_slot + 3;          // (even CTA) stages, or rows of A, that each CTA's loaders began
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    const long long drain_limit = p.wait_limit > 4000000000ll ? p.wait_limit : 4000000000ll;
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
     // this pair's tiles: every step-th, or (AST) consecutive ones
     const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -1492,7 +1517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         mbar_init(smem_u32(drain), 1);
         mbar_init(smem_u32(afull), 1);
         mbar_init(smem_u32(aempty), 1);
-        *abort_flag = 0;
+        *abort_flag = *other_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -1532,11 +1557,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
             __syncwarp();
         }
-        if (!ok && rank == 0 && lane == 0 && rows > 0) mbar_drain(smem_u32(afull), (rows - 1) & 1u, drain_limit);
+        if (lane == 0) store_even(&begun_by[2 * rank], rows);
     } else if (warp == 0 || warp == 2) {
         const bool loads_a = warp == 0;
         int stage = 0;
-        uint32_t phase = 0, armed = 0, armed_parity = 0;
+        uint32_t phase = 0, begun = 0;
         bool ok = true;
         for (int64_t t = first; t < end && ok; t += step) {
             const int m = (int)(t / p.n_tiles), n = (int)(t - (int64_t)m * p.n_tiles);
@@ -1545,8 +1570,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             for (int kb = 0; kb < p.nkb; ++kb) {
                 ok = wait_warp<true>(smem_u32(&empty[stage]), phase ^ 1u, p.wait_limit, p.status, abort_flag);
                 if (!ok) break;
-                armed |= 1u << stage;
-                armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                ++begun;
                 if (elect_one()) {
                     uint8_t* sfb = sSfB + stage * 2 * kAtomBytes;
                     const uint32_t fb = in_even_cta(smem_u32(&full[stage]));
@@ -1575,11 +1599,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
             }
         }
-        // (the even CTA's barriers stand for both CTAs' loads; neither CTA leaves before
-        // the other, see the end)
-        if (!ok && rank == 0 && lane == 0 && (AST || loads_a))
-            for (int s = 0; s < S; ++s)
-                if (armed & (1u << s)) mbar_drain(smem_u32(&full[s]), (armed_parity >> s) & 1u, drain_limit);
+        if (lane == 0) store_even(&begun_by[2 * rank + (loads_a ? 0 : 1)], begun);
     } else if (warp == 1) {
         if (rank == 0) {
             int stage = 0, slot = S - 1;
@@ -1645,12 +1665,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     if (last) ++span;
                 }
             }
-            if (!ok && elect_one()) {
-                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                                 smem_u32(drain))
-                             : "memory");
-                mbar_drain(smem_u32(drain), 0u, drain_limit);
-            }
         } else if (lane == 0) {
             const int64_t spans = first < end ? (end - first + step - 1) / step * ((p.nkb + kSpan - 1) / kSpan) : 0;
             for (int64_t i = 0; i < spans; ++i) {
@@ -1709,8 +1723,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
     tc_fence_before();
     __syncthreads();
-    // neither CTA's shared or tensor memory goes while the other may still use it
+    // neither CTA's shared or tensor memory goes while the other may still use it, nor
+    // while loads or MMAs of a pair that gave up may be in flight (the even CTA's barriers
+    // stand for both CTAs' loads)
+    if (threadIdx.x == 0 && *abort_flag) store_cta(other_abort, rank ^ 1u, 1u);
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (*abort_flag || *other_abort) {
+        if (rank == 0 && threadIdx.x == 0) {
+            const uint32_t a = max(begun_by[0], begun_by[2]), b = max(begun_by[1], begun_by[3]);
+            drain_ring<S>(full, AST ? b : max(a, b), drain_limit(p));
+            if (AST && a > 0) mbar_drain(smem_u32(afull), (a - 1) & 1u, drain_limit(p));
+        }
+        if (rank == 0 && warp == 1 && elect_one()) {
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                             smem_u32(drain))
+                         : "memory");
+            mbar_drain(smem_u32(drain), 0u, drain_limit(p));
+        }
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
