@@ -1,6 +1,9 @@
-"""Every variant of the block8 row kernels, by the rules that choose them: rows on 32 bytes
-(d a multiple of 16), on 16 (of 8), on 8, and on single elements; by slots and in order;
-short calls and those that settle their slots first. Compared bit for bit with the oracle."""
+"""Every variant of the block8 row kernels, and of the products, by the rules that choose
+them: rows on 32 bytes (d a multiple of 16), on 16 (of 8), on 8, and on single elements;
+by slots and in order; short calls and those that settle their slots first.
+
+Rows are compared bit for bit with the oracle. Products are of whole numbers whose sums are
+exact in fp32, or are compared with one another bit for bit: no tolerance."""
 
 import numpy as np
 import pytest
@@ -113,3 +116,63 @@ def test_rows_in_order(em, n, d, kind):
         m.read(out[:n], first=2)
         assert torch.equal(out[:n].cpu(), torch.from_numpy(held).to(dt)), dt
         assert (out[n] == 9).all()
+
+
+# ---------------------------------------------------------------- products without a tolerance
+
+# a result's few rows, few columns, one tile, several, and pairs of CTAs
+RESULTS = [(1, 64), (16, 500), (300, 20), (150, 140), (2000, 1700)]
+
+
+def _product(em, x, y, dtype=torch.float32):
+    A, Bm = em.Block8(*x.shape), em.Block8(*y.shape)
+    A.write(x.cuda())
+    Bm.write(y.cuda())
+    out = torch.empty(len(x), len(y), dtype=dtype, device="cuda")
+    A.matmul(Bm, out)
+    A.check()
+    return out
+
+
+@pytest.mark.parametrize("d", [640, 768, 2049, 5000, 8192, 9000])
+@pytest.mark.parametrize("na,nb", RESULTS)
+def test_whole_numbers_are_multiplied_exactly(em, na, nb, d):
+    """Numbers of -4 .. 4 are held exactly, and all partial sums are below 2^24: every
+    value of a row counts once."""
+    g = np.random.default_rng(d + na)
+    x, y = (g.integers(-4, 5, s).astype(np.float32) for s in ((na, d), (nb, d)))
+    assert 16 * d < 2 ** 24
+    out = _product(em, torch.from_numpy(x), torch.from_numpy(y))
+    want = x.astype(np.float64) @ y.astype(np.float64).T
+    assert np.array_equal(_f64(out), want)
+
+
+@pytest.mark.parametrize("d", [2048, 4096, 8192, 9216, 16384])
+@pytest.mark.parametrize("na,nb", RESULTS)
+def test_small_terms_behind_large_ones_are_kept(em, na, nb, d):
+    """The first 1,024 products of a result are 2^14, which makes 2^24 (times a power of two
+    for each row), and of each 32 after them one is 1 and the others are 0. Added up by 1,024
+    they are whole multiples of fp32's last place there; added to 2^24 one MMA step at a
+    time each would be lost."""
+    x, y = np.zeros((na, d)), np.ones((nb, d))
+    x[:, :1024] = y[:, :1024] = 128
+    x[:, 1024::32] = 1
+    x *= np.exp2(np.arange(na) % 5)[:, None]
+    y *= np.exp2(-(np.arange(nb) % 3))[:, None]
+    out = _product(em, torch.from_numpy(x).float(), torch.from_numpy(y).float())
+    want = x @ y.T
+    assert want[0, 0] == 2 ** 24 + (d - 1024) // 32
+    assert np.array_equal(_f64(out), want)
+
+
+@pytest.mark.parametrize("d", [300, 400, 640, 700, 768])
+def test_pairs_that_keep_their_rows_make_the_same_sums(em, d):
+    """Rows of 3 to 6 blocks, which the pair kernel keeps in shared memory for 16-bit results
+    (of 6 blocks for 32-bit ones): the sums of the single-CTA kernels, rounded once."""
+    g = np.random.default_rng(d)
+    x, y = (torch.from_numpy(g.standard_normal((n, d))).float() for n in (2000, 1700))
+    full = _product(em, x, y)
+    assert torch.equal(_product(em, x[:128], y), full[:128]) and torch.equal(_product(em, x, y[:32]), full[:, :32])
+    assert torch.equal(_product(em, x[300:301], y[:90]), full[300:301, :90])
+    for dt in (torch.bfloat16, torch.float16):
+        assert torch.equal(_product(em, x, y, dt), full.to(dt)), dt
