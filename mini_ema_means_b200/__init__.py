@@ -487,7 +487,10 @@ class Model:
             self._raw_dtype = raw
             torch.cuda.current_stream(X.device).synchronize()  # (the model reads on a stream of its own)
         elif hasattr(X, "dtype"):
-            self.set_option("input_dtype", 1 if "bfloat16" in str(X.dtype) else 0)
+            name = str(X.dtype)
+            if "bfloat16" not in name and "float32" not in name:
+                raise TypeError(f"X must be float32, bfloat16 or a Block8, not {X.dtype}")
+            self.set_option("input_dtype", 1 if "bfloat16" in name else 0)
         elif was == EM_DTYPE_BLOCK8 and self._raw_dtype is not None:
             self.set_option("input_dtype", self._raw_dtype)
 

@@ -188,3 +188,26 @@ def test_binding_refuses_bad_tensors(em):
     assert m.write(torch.zeros(0, 40, dtype=f), stream=0) is None
     assert m.read(torch.zeros(0, 40), stream=0).shape == (0, 40)
     assert m.matmul(m, torch.zeros(0, 3), stream=0).shape == (0, 3)
+
+
+def test_a_model_refuses_data_of_other_types(em):
+    """float16 rows, which a Block8 can be written from, are no input of a model: they would
+    be read as float32, past their end."""
+    class Options:
+        was = 0
+
+        def get_option(self, name):
+            return self.was
+
+        def set_option(self, name, value):
+            self.was = value
+
+    m = Options()
+    m._raw_dtype = None
+    for X, want in ((torch.zeros(3, 4), 0), (torch.zeros(3, 4, dtype=torch.bfloat16), 1), (np.zeros((3, 4), np.float32), 0)):
+        m.was = 7
+        em.Model._dtype_of(m, X)
+        assert m.was == want
+    for X in (torch.zeros(3, 4).half(), torch.zeros(3, 4).double(), torch.zeros(3, 4).long(), np.zeros((3, 4)), np.zeros((3, 4), np.float16)):
+        with pytest.raises(TypeError):
+            em.Model._dtype_of(m, X)
