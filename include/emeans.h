@@ -66,7 +66,9 @@ enum em_option {
     EM_OPT_INPUT_DTYPE = 7,      /* dtype of X: 0 fp32 (default), 1 bf16, 3 a block8 matrix: X is
                                     then a const em_block8_t* (host memory) of d columns and at
                                     least n rows, whose rows [0, n) are read back to bf16 (which
-                                    is exact) inside the call                                   */
+                                    is exact) inside the call, into n x d values of the model's
+                                    own: em_begin and em_lloyd leave them with the model,
+                                    em_assign and em_mse free them at their end                 */
     EM_OPT_CHECK_FINITE = 8,     /* 1: scan X for NaN/Inf in em_begin/em_train (EM_E_NONFINITE) */
     EM_OPT_WAIT_LIMIT_MS = 9,    /* limit of every device-side spin wait, ms (default 2000)    */
     EM_OPT_AUTO_REVIVE = 10,     /* 1 (default): em_step runs the revival check after every 5th
@@ -369,8 +371,8 @@ int em_sync(em_model* m);
  * bounded mbarrier wait on a barrier nothing arrives on, which gives up after
  * wait_ms and returns EM_E_TIMEOUT; which = 1 raises the index-check error and
  * returns EM_E_BOUNDS; which = 3 does as 0 with the wait of the block8 products, by
- * two warps, of which one gives up because the other did. The error word is cleared when reported, so the model stays
- * usable. wait_ms in (0, 10000]. */
+ * two warps, of which one gives up because the other did. The error word is cleared
+ * when reported, so the model stays usable. wait_ms in (0, 10000]. */
 int em_selftest(em_model* m, int which, double wait_ms);
 
 /* The FP8 converter of the model (EM_OPT_SEARCH_FORMAT = 1) fitted by the last

@@ -286,8 +286,10 @@ class Block8:
     memory it uses) and do not wait for it. They are no part of autograd: write takes
     the values of X as if detached, and what the calls write counts as modified in place
     (`out`, `codes`, `scales`), so that a backward pass which saved it refuses. An `out`
-    that requires gradients is refused, but under torch.no_grad(). A Block8 is also an X for Model.train, begin,
-    lloyd, assign and mse, which wait for the current stream of its device first."""
+    that requires gradients is refused, but under torch.no_grad(). A Block8 is also an X
+    for Model.train, begin, lloyd, assign and mse, which wait for the current stream of its
+    device first and read it into a bf16 copy, which train, begin and lloyd leave with the
+    model and assign and mse free at their end."""
 
     def __init__(self, rows, d, device=None, codes=None, scales=None):
         import torch

@@ -152,6 +152,10 @@ __device__ __forceinline__ int64_t slot_of(const int64_t* __restrict__ slots, in
 // entry that this call did not make (its row does not name the slot) is no row of this
 // call, so the array needs no initial value, and a captured call can be replayed at any
 // time. The loop ends, since what it puts back grows.
+// The pass costs a second launch, the scan grows with the rows. Of 768 bf16 values each,
+// in a captured graph: 32 rows 2.5 us with the scan and 3.4 with the pass, 128 3.3 and 3.6,
+// 512 5.8 and 3.6, 1,024 9.5 and 3.7; called one by one, where the host's part of the
+// second launch counts, 512 rows 6.2 and 8.3.
 constexpr int kScanRows = 512;
 
 __global__ void k_block8_claim(const int64_t* __restrict__ slots, int64_t n, int64_t rows, int* __restrict__ claims) {
@@ -468,9 +472,11 @@ __global__ void __launch_bounds__(256)
 // maxima (of 16-bit types two to a word) meet by shuffles and in shared memory; the
 // words are turned in shared memory (16-byte pieces of a row XORed with the row's group
 // of V, which keeps both sides off each other's banks) and leave as 128 bytes per row.
-// 48 registers, so that five blocks share an SM, and a row's exponent is found by one
-// thread: 1,000 rows of 30,001 fp16 values take 19 us (with the values kept as floats,
-// 100 registers, and every thread finding the exponents 46).
+// The values stay in their type and a row's exponent is found by one thread, so that five
+// blocks share an SM on 48 registers (fp32: six, on 40): 1,000 rows of 30,001 fp16 values
+// take 19 us (with the values kept as floats, 100 registers, and every thread finding the
+// exponents 46). Columns whose distance is no multiple of 16 bytes are loaded value by
+// value: 4,095 rows of 16,384 bf16 79 us, 4,096 of them 40 (fp32 61 and 53).
 template <class T>
 struct ColTile {
     static constexpr int V = 16 / (int)sizeof(T);
@@ -726,7 +732,8 @@ __global__ void __launch_bounds__(256, 8)
 // consecutive (row, block) pairs at a time, and a lane the values lane, lane + 32, lane
 // + 64 and lane + 96 of each, so that every store of a warp is one run of neighbours.
 // (With 8 consecutive values per lane, stored one by one, 30,000 rows of 1,581 fp16
-// values took 128 us, and here 79; of 1,579 fp32 values 151 and 57.)
+// values took 132 us in order and 129 by slots, and here 54 and 78; of 1,579 fp32 values
+// 153 and 144, and here 57 and 73.)
 struct BlockPairs {
     int row[kSteps], b[kSteps];
     __device__ __forceinline__ BlockPairs(uint32_t f, const FastDiv& nb) {
@@ -1082,7 +1089,9 @@ __device__ __forceinline__ void store_rows(const uint32_t (&sum)[NS][32], uint8_
 //
 // Long rows with few tiles: a cluster of `split` CTAs shares a tile, one span of the
 // rows each. The spans' results meet in shared memory, and the cluster's first CTA adds
-// them in order: the sums are those of a CTA that does all spans, bit for bit.
+// them in order: the sums are those of a CTA that does all spans, bit for bit. A cluster
+// has at most 8 CTAs; longer rows, and more tiles than SMs / spans, have a CTA to a tile
+// (16 x 512: d = 8,192 7.9 us, 8,193 18.5, 16,384 33; 1,024 x 512 x 16,384 40).
 
 template <int BN, bool SWAP>
 struct MmCfg {
